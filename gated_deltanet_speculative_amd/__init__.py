@@ -23,6 +23,14 @@ and a prompt fills a slot with conv_step over its tokens followed by
                        prefill_noalloc: the same with the library's static scratch,
                        for callers that cannot allocate)
 
+Around the recurrence (include/gdn_round.h), the attention layers' part of a round over a
+paged key/value cache and the acceptance of the draft:
+
+    rope_kv_write    -> q_out; rotary positions, k and v written behind the committed rows
+    paged_attention  -> out; the round's tokens over the cache and their own ancestors
+    draft_accept     -> accept_node, n_accept, next_token (what the commits take)
+    kv_commit_layers -> new_len; the accepted paths' cache rows moved together, every layer
+
 The library is loaded on first use and must have been built
 (`python -m gated_deltanet_speculative_amd.build`); there is no fallback path.
 """
@@ -54,4 +62,19 @@ from ._lib import (  # noqa: F401
     replay_commit_layers,
     strerror,
     tree_verify,
+)
+from ._round import (  # noqa: F401
+    AcceptShape,
+    AttnShape,
+    ROUND_EXPORTED,
+    STATUS_AXIS,
+    STATUS_LENGTH,
+    STATUS_PAGE,
+    STATUS_TOKEN,
+    draft_accept,
+    draft_accept_workspace_size,
+    kv_commit_layers,
+    paged_attention,
+    paged_attention_workspace_size,
+    rope_kv_write,
 )

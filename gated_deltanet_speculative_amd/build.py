@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libgdnverify.so")
 ARCH = "gfx950"
 
 SOURCES = ["gdn_api.cpp", "conv_tree_step.hip", "tree_verify.hip", "replay_commit.hip", "decode_step.hip",
-           "prefill.hip"]
+           "prefill.hip", "round_api.cpp", "rope_kv_write.hip", "paged_attention.hip", "draft_accept.hip",
+           "kv_commit.hip"]
 
 # Packed-FP32 instructions are disabled: the compiler may otherwise fuse ordinary
 # float code into them.

@@ -1,0 +1,520 @@
+// Attention of a round's new tokens over a slot's paged key/value cache, for gfx950.
+//
+// Mathematics.  For node i of a lane and query head h (kv head h / G) with the rows t that i
+// attends to:  x_t = scale q.K[t],  out = sum_t e^{x_t} V[t] / sum_t e^{x_t}.  One pass over the
+// cache keeps, per query row, the running maximum m, the sum l of e^{x - m} and the unnormalised
+// output o; a new block of rows rescales l and o by e^{m_old - m_new} (all in 32 bits).
+//
+// Layout of a workgroup's work.  The query rows of one (lane, kv head) are its N*G pairs
+// (token, head of the group), in that order: they share every K and V row.  A wave owns RT tiles
+// of 16 query rows and computes S^T = K Q^T with 16x16 matrix instructions: the accumulator of
+// a tile holds, in lane l, the scores of query row l % 16 against cache rows 4 (l / 16) + 0..3.  So
+// the softmax statistics of a query row are scalars of its lanes, and the weights are, as they
+// stand, the right operand of O^T = V^T P^T (the contraction runs over cache rows in the order
+// the accumulators hold them, which the left operand follows); no score goes through memory.
+// The left operand V^T takes four cache rows of one column per lane: the 16-bit path reads it
+// with the transposing LDS load, the 32-bit path with plain loads of one value.
+#include "round_device.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr float kNegInf = -__builtin_inff();
+
+// ---- the value types: 16-byte operand fragments and the matrix instructions on them.
+// A fragment holds 64 bytes' worth of one row over the four lane groups: 32 16-bit or 16 32-bit
+// contraction indices per step.
+template <typename T>
+struct Type;
+template <>
+struct Type<__bf16> {
+    static constexpr int kTok = 64;  // cache rows per tile
+    static constexpr unsigned kExp = 0x7f80u;
+    static __device__ v4f mma(v4i a, v4i b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    }
+    static __device__ v4i pack(v4f a, v4f b) {
+        return __builtin_bit_cast(v4i, bf8{(__bf16)a[0], (__bf16)a[1], (__bf16)a[2], (__bf16)a[3], (__bf16)b[0],
+                                           (__bf16)b[1], (__bf16)b[2], (__bf16)b[3]});
+    }
+};
+template <>
+struct Type<_Float16> {
+    static constexpr int kTok = 64;
+    static constexpr unsigned kExp = 0x7c00u;
+    static __device__ v4f mma(v4i a, v4i b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+    static __device__ v4i pack(v4f a, v4f b) {
+        return __builtin_bit_cast(v4i, h8{(_Float16)a[0], (_Float16)a[1], (_Float16)a[2], (_Float16)a[3],
+                                          (_Float16)b[0], (_Float16)b[1], (_Float16)b[2], (_Float16)b[3]});
+    }
+};
+template <>
+struct Type<float> {
+    static constexpr int kTok = 32;
+    static constexpr unsigned kExp = 0x7f800000u;
+    static __device__ v4f mma(v4i a, v4i b, v4f c) { return mfma4(__builtin_bit_cast(v4f, a), __builtin_bit_cast(v4f, b), c); }
+};
+
+// A tile row of D values in LDS is D * sizeof(T) / 16 chunks of 16 bytes; chunk c of row r is kept
+// at place c ^ swizzle(r), so that the 16 rows (or 4 rows of each lane group) that one operand
+// read touches at the same column use distinct banks.
+template <int kRowBytes>
+__device__ inline int swizzle(int r) {
+    return kRowBytes == 128 ? (r >> 1) & 7 : r & 15;
+}
+template <int kRowBytes>
+__device__ inline int lds_at(int r, int chunk) {
+    return r * kRowBytes + ((chunk ^ swizzle<kRowBytes>(r)) << 4);
+}
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+// The left operand of the second product: contraction step u (32 cache rows of a 16-bit tile, 16
+// of a 32-bit one) and output columns 16 dt .. 16 dt + 15.  Slot j = 4t + i of lane group g is cache
+// row 32u + 16t + 4g + i (t = 0 only for 32-bit).
+template <typename T, int D>
+__device__ inline v4i v_operand(const char *vt, int u, int dt, int lane) {
+    constexpr int RB = D * sizeof(T);
+    const int g = lane >> 4, n = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+        typedef int v2i __attribute__((ext_vector_type(2)));
+        v2i part[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int row = 32 * u + 16 * t + 4 * g + (n >> 2);
+            const char *p = vt + lds_at<RB>(row, 2 * dt + ((n & 3) >> 1)) + 8 * (n & 1);
+            part[t] = __builtin_bit_cast(
+                v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
+        }
+        return v4i{part[0][0], part[0][1], part[1][0], part[1][1]};
+    } else {
+        v4i r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = *reinterpret_cast<const int *>(vt + lds_at<RB>(16 * u + 4 * g + i, 4 * dt + (n >> 2)) + 4 * (n & 3));
+        return r;
+    }
+}
+
+// Replaces the values of an operand that are infinite or NaN by zeros; whether there was one.
+template <typename T>
+__device__ inline bool drop_nonfinite(v4i &f) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        unsigned w = (unsigned)f[j];
+        if constexpr (sizeof(T) == 2) {
+            const bool lo = (w & Type<T>::kExp) == Type<T>::kExp, hi = ((w >> 16) & Type<T>::kExp) == Type<T>::kExp;
+            any |= lo | hi;
+            w = (lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u);
+        } else {
+            const bool b = (w & Type<T>::kExp) == Type<T>::kExp;
+            any |= b;
+            w = b ? 0u : w;
+        }
+        f[j] = (int)w;
+    }
+    return any;
+}
+
+__device__ inline float lane_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ inline float lane_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// What rows r0 .. r0 + rows - 1 of a lane's N_c * G query rows attend to at most: cache rows
+// 0 .. end - 1, divided into parts of whole tiles.
+struct Reach {
+    int end, part;
+};
+__device__ inline Reach reach(bool tree, int len, int nodes, int last_token, int splits, int tok) {
+    const int end = len + (tree ? nodes : min(last_token, nodes - 1) + 1);
+    const int tiles = (end + tok - 1) / tok;
+    return Reach{end, (tiles + splits - 1) / splits * tok};
+}
+
+template <typename T>
+__device__ inline void store4(T *p, v4f v) {
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<t4 *>(p) = t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+}
+template <typename T>
+__device__ inline v4f load4(const T *p) {
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    const t4 v = *reinterpret_cast<const t4 *>(p);
+    return v4f{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+__device__ inline float gated(float o, float z, int mode) { return o * (mode == 0 ? fast_silu(z) : fast_sigmoid(z)); }
+
+// Query rows split over the waves (16 RT each), cache tiles shared through LDS: each wave's products
+// read the tile once, so the LDS traffic per product falls with RT.  The next tile's rows are
+// loaded to registers while the current one is worked on, and its page ids a tile earlier.
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int RB = D * sizeof(T), TOK = Type<T>::kTok, NT = TOK / 16, NS = RB / 64, ND = D / 16;
+    constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
+    constexpr int BM = 16 * RT * kWaves, NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
+    __shared__ __attribute__((aligned(16))) char s_k[TOK * RB];
+    __shared__ __attribute__((aligned(16))) char s_v[TOK * RB];
+    __shared__ unsigned long long s_absent;  // cache rows of the tile that lie in no page of the pool
+
+    const AttnDims &d = a.d;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4;
+    const bool tree = a.l.parents != nullptr;
+    // Workgroups that share a (lane, kv head) read the same cache rows: with several row tiles,
+    // consecutive units of work go to one XCD (workgroups are dealt to the 8 XCDs in turn).
+    unsigned b = blockIdx.x;
+    const unsigned units = (unsigned)d.C * d.Hkv * plan.tiles * plan.splits;
+    if (plan.tiles > 1) b = (b & 7) * (gridDim.x >> 3) + (b >> 3);
+    if (b >= units) return;
+    const int split = b % plan.splits;
+    // heavy row tiles of a chain (the last tokens) first
+    const int tile = plan.tiles - 1 - (b / plan.splits) % plan.tiles;
+    const int ch = b / (plan.splits * plan.tiles), h = ch % d.Hkv, c = ch / d.Hkv;
+
+    const Lane ln = paged_lane(d, a.l, c);
+    if (ln.slot == -1) return;
+    int bits = ln.bits;
+    unsigned anc = 0;
+    if (tree && !(bits & GDN_STATUS_NODES)) {
+        bool bad;
+        anc = tree_ancestors(a.l.parents + (int64_t)c * d.N, ln.nodes, bad);
+        if (bad) bits |= GDN_STATUS_PARENT;
+    }
+    if (bits) {
+        if (a.l.status && split == 0 && tile == 0 && h == 0 && tid == 0) atomicOr(a.l.status, bits);
+        return;
+    }
+    const int rows = ln.nodes * d.G, r0 = tile * BM, L = ln.len;
+    if (r0 >= rows) return;
+    const Reach rc = reach(tree, L, ln.nodes, (r0 + BM - 1) / d.G, plan.splits, TOK);
+    const int t0 = split * rc.part, t1 = min(t0 + rc.part, rc.end);
+    if (t0 >= t1) return;
+
+    // ---- this wave's query rows (zeros behind the last one) and what they attend to
+    const int rw = r0 + wave * 16 * RT;
+    const bool working = rw < rows;
+    const int first_token = rw / d.G, last_token = min(rw + 16 * RT - 1, rows - 1) / d.G;
+    v4i qf[RT][NS];
+    int token[RT];
+    unsigned sees[RT];  // tree: the nodes a row attends to
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rw + 16 * rt + (lane & 15);
+        token[rt] = min(r, rows - 1) / d.G;
+        sees[rt] = __shfl(anc, token[rt] & 63);
+        const int gh = min(r, rows - 1) - token[rt] * d.G;
+        const T *q = static_cast<const T *>(a.q) + (((int64_t)c * d.N + token[rt]) * d.Hq + h * d.G + gh) * D;
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) {
+            const v4i v = *reinterpret_cast<const v4i *>(reinterpret_cast<const char *>(q) + 64 * ks + 16 * g);
+            qf[rt][ks] = r < rows ? v : v4i{0, 0, 0, 0};
+        }
+    }
+
+    // ---- staging: thread tid carries chunk tid % TPR of rows tid / TPR + RPP p of the tile
+    const int32_t *table = a.l.page_table + (int64_t)ln.slot * d.max_pages;
+    const int chunk = tid % TPR, row_in = tid / TPR;
+    int pid[NP];
+    v4i kr[NP], vr[NP];
+    unsigned long long absent = 0;
+    auto lookup = [&](int t) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int tk = t + row_in + RPP * p;
+            pid[p] = tk < t1 ? table[d.page((uint32_t)tk)] : -2;
+        }
+    };
+    auto load = [&](int t) {
+        absent = 0;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            kr[p] = vr[p] = v4i{0, 0, 0, 0};
+            const uint32_t tk = t + row_in + RPP * p;
+            if ((unsigned)pid[p] < (unsigned)d.n_pages) {
+                const size_t at = (size_t)cache_row(d, pid[p], h, tk, d.page(tk)) * RB + chunk * 16;
+                kr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at);
+                vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
+            } else if (pid[p] != -2 || tk < (uint32_t)t1) {
+                absent |= 1ull << (row_in + RPP * p);
+            }
+        }
+    };
+
+    v4f o[RT][ND];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kNegInf;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    lookup(t0);
+    load(t0);
+    lookup(t0 + TOK);
+    for (int t = t0; t < t1; t += TOK) {
+        __syncthreads();  // the previous tile has been read
+        if (tid == 0) s_absent = 0;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int at = lds_at<RB>(row_in + RPP * p, chunk);
+            *reinterpret_cast<v4i *>(s_k + at) = kr[p];
+            *reinterpret_cast<v4i *>(s_v + at) = vr[p];
+        }
+        const unsigned long long mine = absent;
+        if (t + TOK < t1) {
+            load(t + TOK);
+            lookup(t + 2 * TOK);
+        }
+        __syncthreads();
+        const bool some_absent = __syncthreads_or(mine != 0);
+        unsigned long long gone = 0;
+        if (some_absent) {  // (no page for these rows: not attended, reported)
+            if (mine) atomicOr(&s_absent, mine);
+            if (tid == 0 && a.l.status) atomicOr(a.l.status, GDN_STATUS_PAGE);
+            __syncthreads();
+            gone = s_absent;
+        }
+        if (!working || (!tree && t > L + last_token)) continue;  // nothing of this tile for this wave
+
+        // ---- S^T = K Q^T
+        v4f s[RT][NT];
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) s[rt][tt] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < NS; ++ks) {
+                const v4i kf = *reinterpret_cast<const v4i *>(s_k + lds_at<RB>(16 * tt + (lane & 15), 4 * ks + g));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) s[rt][tt] = Type<T>::mma(kf, qf[rt][ks], s[rt][tt]);
+            }
+        }
+        // ---- rows that are not attended weigh nothing, whatever their scores are
+        const int all_see = tree ? L : L + first_token + 1;  // rows in front of this: seen by every row of the wave
+        const bool partial = t + TOK > min(all_see, t1) || gone != 0;
+        auto attends = [&](int rt, int at) {
+            const int n = at - L;
+            return at < t1 && !((gone >> (at - t)) & 1) &&
+                   (n < 0 || (tree ? n < GDN_MAX_NODES && ((sees[rt] >> n) & 1) : n <= token[rt]));
+        };
+        if (partial) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!attends(rt, t + 16 * tt + 4 * g + i)) s[rt][tt][i] = kNegInf;
+        }
+        // ---- running maximum and sum; the sum keeps the weights unrounded
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float mx = kNegInf;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[rt][tt][i]);
+            mx = fmaxf(m[rt], lane_max(mx) * a.scale_log2);
+            const float base = mx == kNegInf ? 0.f : mx;  // nothing attended yet: every weight is 2^-inf
+            const float shrink = __builtin_amdgcn_exp2f(m[rt] - base);
+            m[rt] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[rt][tt][i] = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], a.scale_log2, -base));
+                    sum += s[rt][tt][i];
+                }
+            l[rt] = fmaf(l[rt], shrink, sum);
+            if (__builtin_amdgcn_ballot_w64(shrink != 1.f))
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
+        }
+        // ---- O^T += V^T P^T
+        bool strange = false;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            v4i pf[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (sizeof(T) == 2)
+                    pf[rt] = Type<T>::pack(s[rt][2 * u], s[rt][2 * u + 1]);
+                else
+                    pf[rt] = __builtin_bit_cast(v4i, s[rt][u]);
+            }
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) {
+                v4i vf = v_operand<T, D>(s_v, u, dt, lane);
+                if (partial) strange |= drop_nonfinite<T>(vf);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf, pf[rt], o[rt][dt]);
+            }
+        }
+        // A weight of zero times an infinity or NaN is NaN: in a tile with rows that are not
+        // attended such values were left out above and go to the rows that do attend to them.
+        if (partial && __builtin_amdgcn_ballot_w64(strange)) {
+            for (int tk = 0; tk < TOK; ++tk)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    if (!attends(rt, t + tk)) continue;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 16 * dt + 4 * g + i, byte = e * (int)sizeof(T);
+                            const float v = (float)*reinterpret_cast<const T *>(s_v + lds_at<RB>(tk, byte >> 4) + (byte & 15));
+                            if (!__builtin_isfinite(v)) o[rt][dt][i] += v;
+                        }
+                }
+        }
+    }
+
+    // ---- results: lane holds columns 16 dt + 4g .. + 3 of its query row
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rw + 16 * rt + (lane & 15);
+        const float sum = lane_sum(l[rt]);
+        if (r >= rows) continue;
+        if (plan.splits > 1) {  // unnormalised part: [split][row][D], then (maximum, sum) per row
+            const size_t row = (size_t)split * all_rows + ((size_t)c * d.Hkv + h) * d.N * d.G + r;
+            float *po = a.workspace + row * D;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) *reinterpret_cast<v4f *>(po + 16 * dt + 4 * g) = o[rt][dt];
+            if (g == 0) {
+                float *ml = a.workspace + plan.splits * all_rows * D + row * 2;
+                ml[0] = m[rt];
+                ml[1] = sum;
+            }
+            continue;
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const int64_t node = (int64_t)c * d.N + token[rt];
+        const int head = h * d.G + r - token[rt] * d.G;
+        T *out = static_cast<T *>(a.out) + (node * d.Hq + head) * D;
+        const T *z = static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) {
+            v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o[rt][dt] * inv;
+            if (a.gate.p) {
+                const v4f zz = load4(z + 16 * dt + 4 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = gated(v[i], zz[i], a.gate_mode);
+            }
+            store4(out + 16 * dt + 4 * g, v);
+        }
+    }
+}
+
+// Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int TOK = Type<T>::kTok, W = D / 64;
+    typedef float vw __attribute__((ext_vector_type(W)));
+    typedef T tw __attribute__((ext_vector_type(W)));
+    const AttnDims &d = a.d;
+    const int lane = threadIdx.x & 63;
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (row >= all_rows) return;
+    const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
+    const bool tree = a.l.parents != nullptr;
+    const Lane ln = paged_lane(d, a.l, c);
+    if (ln.slot == -1 || ln.bits || r >= ln.nodes * d.G) return;
+    if (tree) {
+        bool bad;
+        tree_ancestors(a.l.parents + (int64_t)c * d.N, ln.nodes, bad);
+        if (bad) return;
+    }
+    const int bm = plan.rows_per_group;
+    const Reach rc = reach(tree, ln.len, ln.nodes, (r / bm * bm + bm - 1) / d.G, plan.splits, TOK);
+    const int parts = (rc.end + rc.part - 1) / rc.part;
+    const float *ml = a.workspace + plan.splits * all_rows * D + row * 2, *po = a.workspace + row * D + lane * W;
+    const float mine = lane < parts ? ml[lane * all_rows * 2] : kNegInf;
+    const float part_sum = lane < parts ? ml[lane * all_rows * 2 + 1] : 0.f;
+    float mx = mine;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
+    // (a part without any attended row has weight 0; NaN sums stay NaN)
+    const float wgt = mine == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mine - mx);
+    float sum = part_sum == 0.f ? 0.f : part_sum * wgt;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
+    vw acc = 0.f;
+    constexpr int kAhead = 8;  // parts loaded together
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+        vw v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            v[j] = *reinterpret_cast<const vw *>(po + (size_t)min(p0 + j, parts - 1) * all_rows * D);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const float w = p0 + j < parts ? __shfl(wgt, p0 + j) : 0.f;
+            if (w != 0.f) acc += v[j] * w;
+        }
+    }
+    const int token = r / d.G, head = h * d.G + r - token * d.G;
+    const int64_t node = (int64_t)c * d.N + token;
+    acc = sum == 0.f ? vw(0.f) : acc / sum;
+    if (a.gate.p) {
+        const tw z = *reinterpret_cast<const tw *>(static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head + lane * W);
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] = gated(acc[i], (float)z[i], a.gate_mode);
+    }
+    tw res;
+#pragma unroll
+    for (int i = 0; i < W; ++i) res[i] = (T)acc[i];
+    *reinterpret_cast<tw *>(static_cast<T *>(a.out) + (node * d.Hq + head) * D + lane * W) = res;
+}
+
+template <typename T, int D>
+hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
+    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
+    hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, dim3(kThreads), 0, stream, a, p);
+    if (p.splits > 1) {
+        const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
+        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                           stream, a, p);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    if (a.d.D == 64) return launch<T, 64>(a, p, stream);
+    if (a.d.D == 128) return launch<T, 128>(a, p, stream);
+    return launch<T, 256>(a, p, stream);
+}
+
+}  // namespace
+
+AttnPlan attn_plan(const AttnDims &d) {
+    AttnPlan p;
+    p.rows_per_group = 64;
+    p.tiles = (int)(((int64_t)d.N * d.G + p.rows_per_group - 1) / p.rows_per_group);
+    const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
+    const int64_t most = ((int64_t)d.max_pages * d.page.d + 255) / 256;  // parts of at least 256 rows
+    int64_t s = groups >= 512 ? 1 : (1024 + groups - 1) / groups;
+    if (s > most) s = most;
+    p.splits = (int)(s > 64 ? 64 : s);
+    return p;
+}
+
+hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t stream) {
+    const AttnPlan p = attn_plan(a.d);
+    if (a.d.dtype == GDN_DTYPE_BF16) return launch_t<__bf16>(a, p, stream);
+    if (a.d.dtype == GDN_DTYPE_F16) return launch_t<_Float16>(a, p, stream);
+    return launch_t<float>(a, p, stream);
+}
+
+}  // namespace gdn
