@@ -14,6 +14,8 @@
 // the accumulators hold them, which the left operand follows); no score goes through memory.
 // The left operand V^T takes four cache rows of one column per lane: the 16-bit path reads it
 // with the transposing LDS load, the 32-bit path with plain loads of one value.
+#include <type_traits>
+
 #include "round_device.h"
 
 namespace gdn {
@@ -30,7 +32,7 @@ struct Type;
 template <>
 struct Type<__bf16> {
     static constexpr int kTok = 64;  // cache rows per tile
-    static constexpr unsigned kExp = 0x7f80u;
+    static constexpr unsigned kExp = 0x7f80u, kOne = 0x3f80u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     }
@@ -42,7 +44,7 @@ struct Type<__bf16> {
 template <>
 struct Type<_Float16> {
     static constexpr int kTok = 64;
-    static constexpr unsigned kExp = 0x7c00u;
+    static constexpr unsigned kExp = 0x7c00u, kOne = 0x3c00u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
     }
@@ -54,7 +56,7 @@ struct Type<_Float16> {
 template <>
 struct Type<float> {
     static constexpr int kTok = 32;
-    static constexpr unsigned kExp = 0x7f800000u;
+    static constexpr unsigned kExp = 0x7f800000u, kOne = 0x3f800000u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) { return mfma4(__builtin_bit_cast(v4f, a), __builtin_bit_cast(v4f, b), c); }
 };
 
@@ -105,20 +107,39 @@ __device__ inline bool drop_nonfinite(v4i &f) {
     bool any = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        unsigned w = (unsigned)f[j];
+        const unsigned w = (unsigned)f[j];
         if constexpr (sizeof(T) == 2) {
             const bool lo = (w & Type<T>::kExp) == Type<T>::kExp, hi = ((w >> 16) & Type<T>::kExp) == Type<T>::kExp;
             any |= lo | hi;
-            w = (lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u);
+            f[j] = (int)((lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u));
         } else {
             const bool b = (w & Type<T>::kExp) == Type<T>::kExp;
             any |= b;
-            w = b ? 0u : w;
+            f[j] = b ? 0 : (int)w;
         }
-        f[j] = (int)w;
     }
     return any;
 }
+
+// One where a value is infinite with this sign, or NaN; zero elsewhere.
+template <typename T>
+__device__ inline v4i nonfinite_ones(v4i f, bool negative) {
+    constexpr unsigned E = Type<T>::kExp, S = sizeof(T) == 2 ? 0x8000u : 0x80000000u, one = Type<T>::kOne;
+    auto is = [&](unsigned x) { return (x & E) == E && ((x & (S - 1u)) != E || ((x & S) != 0) == negative); };
+    v4i r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const unsigned w = (unsigned)f[j];
+        if constexpr (sizeof(T) == 2)
+            r[j] = (int)((is(w & 0xffffu) ? one : 0u) | (is(w >> 16) ? one << 16 : 0u));
+        else
+            r[j] = (int)(is(w) ? one : 0u);
+    }
+    return r;
+}
+
+// The lowest k bits, k of any sign and size
+__device__ inline unsigned long long low_bits(int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull; }
 
 __device__ inline float lane_max(float x) {
     x = fmaxf(x, __shfl_xor(x, 16));
@@ -154,16 +175,18 @@ __device__ inline v4f load4(const T *p) {
 __device__ inline float gated(float o, float z, int mode) { return o * (mode == 0 ? fast_silu(z) : fast_sigmoid(z)); }
 
 // Query rows split over the waves (16 RT each), cache tiles shared through LDS: each wave's products
-// read the tile once, so the LDS traffic per product falls with RT.  The next tile's rows are
-// loaded to registers while the current one is worked on, and its page ids a tile earlier.
+// read the tile once, so the LDS traffic per product falls with RT.  Two tiles of LDS, one barrier
+// per tile: the next tile's rows are loaded to registers while the current one is worked on (its page
+// ids a tile earlier) and written to the other half before the barrier.
 template <typename T, int D, int RT>
-__global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = Type<T>::kTok, NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
     constexpr int BM = 16 * RT * kWaves, NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
-    __shared__ __attribute__((aligned(16))) char s_k[TOK * RB];
-    __shared__ __attribute__((aligned(16))) char s_v[TOK * RB];
-    __shared__ unsigned long long s_absent;  // cache rows of the tile that lie in no page of the pool
+    __shared__ __attribute__((aligned(16))) char s_kv[2][2][TOK * RB];
+    // cache rows of a tile that lie in no page of the pool: by tile number mod 3 (written before the
+    // tile's barrier, read behind it, cleared before the barrier of the second tile after it)
+    __shared__ unsigned long long s_absent[3];
 
     const AttnDims &d = a.d;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4;
@@ -224,27 +247,27 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPla
     const int chunk = tid % TPR, row_in = tid / TPR;
     int pid[NP];
     v4i kr[NP], vr[NP];
-    unsigned long long absent = 0;
     auto lookup = [&](int t) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int tk = t + row_in + RPP * p;
-            pid[p] = tk < t1 ? table[d.page((uint32_t)tk)] : -2;
+            pid[p] = table[d.page((uint32_t)min(tk, t1 - 1))];
+            pid[p] = tk < t1 ? pid[p] : -1;
         }
     };
+    // (a row without a page is loaded from the pool's first row and cleared before it is used)
+    unsigned unpaged = 0;
     auto load = [&](int t) {
-        absent = 0;
+        unpaged = 0;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            kr[p] = vr[p] = v4i{0, 0, 0, 0};
             const uint32_t tk = t + row_in + RPP * p;
-            if ((unsigned)pid[p] < (unsigned)d.n_pages) {
-                const size_t at = (size_t)cache_row(d, pid[p], h, tk, d.page(tk)) * RB + chunk * 16;
-                kr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at);
-                vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
-            } else if (pid[p] != -2 || tk < (uint32_t)t1) {
-                absent |= 1ull << (row_in + RPP * p);
-            }
+            const bool ok = (unsigned)pid[p] < (unsigned)d.n_pages;
+            const uint32_t row = ok ? cache_row(d, pid[p], h, tk, d.page(tk)) : 0u;
+            unpaged |= ok ? 0u : 1u << p;
+            const size_t at = (size_t)row * RB + chunk * 16;
+            kr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at);
+            vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
         }
     };
 
@@ -257,34 +280,9 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPla
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    lookup(t0);
-    load(t0);
-    lookup(t0 + TOK);
-    for (int t = t0; t < t1; t += TOK) {
-        __syncthreads();  // the previous tile has been read
-        if (tid == 0) s_absent = 0;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int at = lds_at<RB>(row_in + RPP * p, chunk);
-            *reinterpret_cast<v4i *>(s_k + at) = kr[p];
-            *reinterpret_cast<v4i *>(s_v + at) = vr[p];
-        }
-        const unsigned long long mine = absent;
-        if (t + TOK < t1) {
-            load(t + TOK);
-            lookup(t + 2 * TOK);
-        }
-        __syncthreads();
-        const bool some_absent = __syncthreads_or(mine != 0);
-        unsigned long long gone = 0;
-        if (some_absent) {  // (no page for these rows: not attended, reported)
-            if (mine) atomicOr(&s_absent, mine);
-            if (tid == 0 && a.l.status) atomicOr(a.l.status, GDN_STATUS_PAGE);
-            __syncthreads();
-            gone = s_absent;
-        }
-        if (!working || (!tree && t > L + last_token)) continue;  // nothing of this tile for this wave
-
+    // One tile for this wave.  `masked`: some row does not attend to some of it.
+    auto work = [&](auto masked, const char *s_k, const char *s_v, int t, unsigned long long gone) {
+        constexpr bool kMasked = decltype(masked)::value;
         // ---- S^T = K Q^T
         v4f s[RT][NT];
 #pragma unroll
@@ -298,22 +296,26 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPla
                 for (int rt = 0; rt < RT; ++rt) s[rt][tt] = Type<T>::mma(kf, qf[rt][ks], s[rt][tt]);
             }
         }
-        // ---- rows that are not attended weigh nothing, whatever their scores are
-        const int all_see = tree ? L : L + first_token + 1;  // rows in front of this: seen by every row of the wave
-        const bool partial = t + TOK > min(all_see, t1) || gone != 0;
-        auto attends = [&](int rt, int at) {
-            const int n = at - L;
-            return at < t1 && !((gone >> (at - t)) & 1) &&
-                   (n < 0 || (tree ? n < GDN_MAX_NODES && ((sees[rt] >> n) & 1) : n <= token[rt]));
-        };
-        if (partial) {
+        // ---- rows that are not attended weigh nothing, whatever their scores are: the tile's rows that a query
+        // row attends to as a bit set, shifted so that this lane's rows are bits 16 tt + i
+        unsigned long long see[RT];
+        if constexpr (kMasked) {
+            int g4 = 4 * g;
+            asm volatile("" : "+v"(g4));  // (keeps what follows out of the other tiles' registers)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RT; ++rt) {
+                const int rel = L - t;
+                unsigned long long x = low_bits(min(tree ? rel : rel + token[rt] + 1, t1 - t));
+                if (tree) {
+                    const unsigned long long nodes = sees[rt];
+                    x |= (rel >= 64 || rel <= -32 ? 0 : rel >= 0 ? nodes << rel : nodes >> -rel) & low_bits(t1 - t);
+                }
+                see[rt] = (x & ~gone) >> g4;
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!attends(rt, t + 16 * tt + 4 * g + i)) s[rt][tt][i] = kNegInf;
+                    for (int i = 0; i < 4; ++i) s[rt][tt][i] = (see[rt] >> (16 * tt + i)) & 1 ? s[rt][tt][i] : kNegInf;
+            }
         }
         // ---- running maximum and sum; the sum keeps the weights unrounded
 #pragma unroll
@@ -355,28 +357,92 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, AttnPla
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) {
                 v4i vf = v_operand<T, D>(s_v, u, dt, lane);
-                if (partial) strange |= drop_nonfinite<T>(vf);
+                if constexpr (kMasked) strange |= drop_nonfinite<T>(vf);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf, pf[rt], o[rt][dt]);
             }
         }
-        // A weight of zero times an infinity or NaN is NaN: in a tile with rows that are not
-        // attended such values were left out above and go to the rows that do attend to them.
-        if (partial && __builtin_amdgcn_ballot_w64(strange)) {
-            for (int tk = 0; tk < TOK; ++tk)
+        // A weight of zero times an infinity or NaN is NaN: such values were left out above.  They go to the
+        // rows that do attend to them by two products of ones (values of +inf or NaN, of -inf or NaN) with
+        // ones (rows attended): a positive count adds +inf, -inf, and both together NaN.
+        if constexpr (kMasked)
+            if (__builtin_amdgcn_ballot_w64(strange)) {
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {
+                    const float inf = side ? kNegInf : -kNegInf;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if (!attends(rt, t + tk)) continue;
+                    for (int u = 0; u < NU; ++u) {
+                        v4i reads[RT];
 #pragma unroll
-                    for (int dt = 0; dt < ND; ++dt)
+                        for (int rt = 0; rt < RT; ++rt) {
+                            float one[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = 16 * dt + 4 * g + i, byte = e * (int)sizeof(T);
-                            const float v = (float)*reinterpret_cast<const T *>(s_v + lds_at<RB>(tk, byte >> 4) + (byte & 15));
-                            if (!__builtin_isfinite(v)) o[rt][dt][i] += v;
+                            for (int j = 0; j < 8; ++j)
+                                one[j] = (see[rt] >> ((sizeof(T) == 2 ? 32 * u + 16 * (j >> 2) : 16 * u) + (j & 3))) & 1 ? 1.f : 0.f;
+                            const v4f lo{one[0], one[1], one[2], one[3]}, hi{one[4], one[5], one[6], one[7]};
+                            if constexpr (sizeof(T) == 2)
+                                reads[rt] = Type<T>::pack(lo, hi);
+                            else
+                                reads[rt] = __builtin_bit_cast(v4i, lo);
                         }
+#pragma unroll
+                        for (int dt = 0; dt < ND; ++dt) {
+                            const v4i vf = nonfinite_ones<T>(v_operand<T, D>(s_v, u, dt, lane), side);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                const v4f n = Type<T>::mma(vf, reads[rt], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[rt][dt][i] += n[i] > 0.f ? inf : 0.f;
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                 }
+            }
+    };
+
+    if (tid < 3) s_absent[tid] = 0;
+    lookup(t0);
+    load(t0);
+    lookup(t0 + TOK);
+    lds_barrier();
+    for (int t = t0, n3 = 0, half = 0; t < t1; t += TOK, half ^= 1) {
+        char *s_k = s_kv[half][0], *s_v = s_kv[half][1];
+        if (unpaged) {
+            unsigned long long absent = 0;  // rows of this part without a page: not attended, reported
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                if ((unpaged >> p) & 1) {
+                    kr[p] = vr[p] = v4i{0, 0, 0, 0};
+                    absent |= t + row_in + RPP * p < t1 ? 1ull << (row_in + RPP * p) : 0ull;
+                }
+            if (absent) {
+                atomicOr(&s_absent[n3], absent);
+                if (a.l.status) atomicOr(a.l.status, GDN_STATUS_PAGE);
+            }
         }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int at = lds_at<RB>(row_in + RPP * p, chunk);
+            *reinterpret_cast<v4i *>(s_k + at) = kr[p];
+            *reinterpret_cast<v4i *>(s_v + at) = vr[p];
+        }
+        const int n3_here = n3;
+        n3 = n3 == 2 ? 0 : n3 + 1;
+        if (tid == 0) s_absent[n3] = 0;
+        if (t + TOK < t1) {
+            load(t + TOK);
+            lookup(t + 2 * TOK);
+        }
+        lds_barrier();
+        const unsigned long long gone = s_absent[n3_here];
+        if (!working || (!tree && t > L + last_token)) continue;  // nothing of this tile for this wave
+
+        const int all_see = tree ? L : L + first_token + 1;  // rows in front of this: seen by every row of the wave
+        if (t + TOK > min(all_see, t1) || gone != 0)
+            work(std::true_type{}, s_k, s_v, t, gone);
+        else
+            work(std::false_type{}, s_k, s_v, t, gone);
     }
 
     // ---- results: lane holds columns 16 dt + 4g .. + 3 of its query row
@@ -480,7 +546,10 @@ template <typename T, int D>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
     const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
-    hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, dim3(kThreads), 0, stream, a, p);
+    if (p.rows_per_group == 64)
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, dim3(kThreads), 0, stream, a, p);
+    else
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, 2>), grid, dim3(kThreads), 0, stream, a, p);
     if (p.splits > 1) {
         const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
         hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
@@ -500,7 +569,7 @@ hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
 
 AttnPlan attn_plan(const AttnDims &d) {
     AttnPlan p;
-    p.rows_per_group = 64;
+    p.rows_per_group = (int64_t)d.N * d.G > 64 ? 128 : 64;
     p.tiles = (int)(((int64_t)d.N * d.G + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
     const int64_t most = ((int64_t)d.max_pages * d.page.d + 255) / 256;  // parts of at least 256 rows
