@@ -21,7 +21,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr float kNegInf = -__builtin_inff();
 
 // ---- the value types: 16-byte operand fragments and the matrix instructions on them.
@@ -31,7 +30,6 @@ template <typename T>
 struct Type;
 template <>
 struct Type<__bf16> {
-    static constexpr int kTok = 64;  // cache rows per tile
     static constexpr unsigned kExp = 0x7f80u, kOne = 0x3f80u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
@@ -43,7 +41,6 @@ struct Type<__bf16> {
 };
 template <>
 struct Type<_Float16> {
-    static constexpr int kTok = 64;
     static constexpr unsigned kExp = 0x7c00u, kOne = 0x3c00u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
@@ -55,10 +52,16 @@ struct Type<_Float16> {
 };
 template <>
 struct Type<float> {
-    static constexpr int kTok = 32;
     static constexpr unsigned kExp = 0x7f800000u, kOne = 0x3f800000u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) { return mfma4(__builtin_bit_cast(v4f, a), __builtin_bit_cast(v4f, b), c); }
 };
+
+// Cache rows of a tile: 16 KiB of K and as much of V, at most 64 rows (a set of them is 64 bits).
+constexpr int tile_rows(int row_bytes) { return row_bytes < 256 ? 64 : 16384 / row_bytes; }
+// Waves of a workgroup of the row kernel.  Rows of 512 bytes and more leave a wave room for one tile of 16
+// query rows only (its outputs and queries alone are 96 registers and more): eight waves share a tile then,
+// so that the tile's loads and staging registers are shared by as many query rows.
+constexpr int row_waves(int row_bytes) { return row_bytes >= 512 ? 8 : 4; }
 
 // A tile row of D values in LDS is D * sizeof(T) / 16 chunks of 16 bytes; chunk c of row r is kept
 // at place c ^ swizzle(r), so that the 16 rows (or 4 rows of each lane group) that one operand
@@ -179,8 +182,8 @@ __device__ inline float gated(float o, float z, int mode) { return o * (mode == 
 // per tile: the next tile's rows are loaded to registers while the current one is worked on (its page
 // ids a tile earlier) and written to the other half before the barrier.
 template <typename T, int D, int RT>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
-    constexpr int RB = D * sizeof(T), TOK = Type<T>::kTok, NT = TOK / 16, NS = RB / 64, ND = D / 16;
+__global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = row_waves(RB), kThreads = 64 * kWaves, NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
     constexpr int BM = 16 * RT * kWaves, NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
     __shared__ __attribute__((aligned(16))) char s_kv[2][2][TOK * RB];
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
     // ---- this wave's query rows (zeros behind the last one) and what they attend to
     const int rw = r0 + wave * 16 * RT;
     const bool working = rw < rows;
-    const int first_token = rw / d.G, last_token = min(rw + 16 * RT - 1, rows - 1) / d.G;
+    const int last_token = min(rw + 16 * RT - 1, rows - 1) / d.G;
     v4i qf[RT][NS];
     int token[RT];
     unsigned sees[RT];  // tree: the nodes a row attends to
@@ -317,7 +320,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
                     for (int i = 0; i < 4; ++i) s[rt][tt][i] = (see[rt] >> (16 * tt + i)) & 1 ? s[rt][tt][i] : kNegInf;
             }
         }
-        // ---- running maximum and sum; the sum keeps the weights unrounded
+        // ---- running maximum and sum; the sum keeps the weights unrounded.  The base of the exponentials follows
+        // the maximum only when that has grown by more than 2^kSlack: weights up to 2^kSlack lose nothing (their
+        // relative rounding is the same), and most tiles need no rescaling of o.
+        constexpr float kSlack = 6.f;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float mx = kNegInf;
@@ -325,10 +331,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
             for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[rt][tt][i]);
-            mx = fmaxf(m[rt], lane_max(mx) * a.scale_log2);
-            const float base = mx == kNegInf ? 0.f : mx;  // nothing attended yet: every weight is 2^-inf
-            const float shrink = __builtin_amdgcn_exp2f(m[rt] - base);
-            m[rt] = mx;
+            mx = lane_max(mx) * a.scale_log2;
+            if (__builtin_amdgcn_ballot_w64(mx > m[rt] + kSlack || (mx > m[rt] && m[rt] == kNegInf))) {
+                const float to = fmaxf(m[rt], mx), base = to == kNegInf ? 0.f : to;
+                const float shrink = __builtin_amdgcn_exp2f(m[rt] - base);
+                m[rt] = to;
+                l[rt] *= shrink;
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
+            }
+            const float base = m[rt] == kNegInf ? 0.f : m[rt];  // nothing attended yet: every weight is 2^-inf
             float sum = 0.f;
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt)
@@ -337,10 +349,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
                     s[rt][tt][i] = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], a.scale_log2, -base));
                     sum += s[rt][tt][i];
                 }
-            l[rt] = fmaf(l[rt], shrink, sum);
-            if (__builtin_amdgcn_ballot_w64(shrink != 1.f))
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
+            l[rt] += sum;
         }
         // ---- O^T += V^T P^T
         bool strange = false;
@@ -406,8 +415,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
     load(t0);
     lookup(t0 + TOK);
     lds_barrier();
-    for (int t = t0, n3 = 0, half = 0; t < t1; t += TOK, half ^= 1) {
-        char *s_k = s_kv[half][0], *s_v = s_kv[half][1];
+    // Writes the loaded tile to LDS, requests the next one and waits for the workgroup: the tile's absent rows.
+    int n3 = 0;
+    auto turn = [&](int t, char *s_k, char *s_v) {
         if (unpaged) {
             unsigned long long absent = 0;  // rows of this part without a page: not attended, reported
 #pragma unroll
@@ -427,7 +437,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
             *reinterpret_cast<v4i *>(s_k + at) = kr[p];
             *reinterpret_cast<v4i *>(s_v + at) = vr[p];
         }
-        const int n3_here = n3;
+        const int here = n3;
         n3 = n3 == 2 ? 0 : n3 + 1;
         if (tid == 0) s_absent[n3] = 0;
         if (t + TOK < t1) {
@@ -435,14 +445,26 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
             lookup(t + 2 * TOK);
         }
         lds_barrier();
-        const unsigned long long gone = s_absent[n3_here];
-        if (!working || (!tree && t > L + last_token)) continue;  // nothing of this tile for this wave
-
-        const int all_see = tree ? L : L + first_token + 1;  // rows in front of this: seen by every row of the wave
-        if (t + TOK > min(all_see, t1) || gone != 0)
-            work(std::true_type{}, s_k, s_v, t, gone);
-        else
-            work(std::false_type{}, s_k, s_v, t, gone);
+        return s_absent[here];
+    };
+    // First the tiles that every row of the workgroup attends to throughout, without a trace of the masks; from
+    // the first other one on (the diagonal, the draft tree, a row without a page) the tiles with masks.
+    const int all_see = min(tree ? L : L + r0 / d.G + 1, t1);
+    int t = t0, half = 0;
+    unsigned long long gone = 0;
+    bool turned = false;
+    for (; t + TOK <= all_see; t += TOK, half ^= 1) {
+        gone = turn(t, s_kv[half][0], s_kv[half][1]);
+        if (gone) {
+            turned = true;
+            break;
+        }
+        if (working) work(std::false_type{}, s_kv[half][0], s_kv[half][1], t, 0ull);
+    }
+    for (; t < t1; t += TOK, half ^= 1) {
+        if (!turned) gone = turn(t, s_kv[half][0], s_kv[half][1]);
+        turned = false;
+        if (working && (tree || t <= L + last_token)) work(std::true_type{}, s_kv[half][0], s_kv[half][1], t, gone);
     }
 
     // ---- results: lane holds columns 16 dt + 4g .. + 3 of its query row
@@ -482,15 +504,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
     }
 }
 
+constexpr int kJoinWaves = 4;
 // Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
-    constexpr int TOK = Type<T>::kTok, W = D / 64;
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int TOK = tile_rows(D * sizeof(T)), W = D / 64;
     typedef float vw __attribute__((ext_vector_type(W)));
     typedef T tw __attribute__((ext_vector_type(W)));
     const AttnDims &d = a.d;
     const int lane = threadIdx.x & 63;
-    const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
     if (row >= all_rows) return;
     const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
     const bool tree = a.l.parents != nullptr;
@@ -544,16 +567,17 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, AttnPla
 
 template <typename T, int D>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    constexpr int RB = D * sizeof(T), kWaves = row_waves(RB);
     const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
-    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
-    if (p.rows_per_group == 64)
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, dim3(kThreads), 0, stream, a, p);
-    else
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, 2>), grid, dim3(kThreads), 0, stream, a, p);
+    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units), block(64 * kWaves);
+    if (p.rows_per_group == 16 * kWaves)
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, block, 0, stream, a, p);
+    else if constexpr (kWaves == 4)
+        hipLaunchKernelGGL((attn_rows_kernel<T, D, 2>), grid, block, 0, stream, a, p);
     if (p.splits > 1) {
         const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
-        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                           stream, a, p);
+        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
+                           dim3(64 * kJoinWaves), 0, stream, a, p);
     }
     return hipGetLastError();
 }
@@ -569,7 +593,8 @@ hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
 
 AttnPlan attn_plan(const AttnDims &d) {
     AttnPlan p;
-    p.rows_per_group = (int64_t)d.N * d.G > 64 ? 128 : 64;
+    const int waves = row_waves(d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2));
+    p.rows_per_group = waves == 4 && (int64_t)d.N * d.G <= 64 ? 64 : 128;
     p.tiles = (int)(((int64_t)d.N * d.G + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
     const int64_t most = ((int64_t)d.max_pages * d.page.d + 255) / 256;  // parts of at least 256 rows
