@@ -22,6 +22,9 @@ namespace gdn {
 namespace {
 
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 6.f;  // how far, in powers of two, a running maximum may lead its base
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 // ---- the value types: 16-byte operand fragments and the matrix instructions on them.
 // A fragment holds 64 bytes' worth of one row over the four lane groups: 32 16-bit or 16 32-bit
@@ -34,6 +37,10 @@ struct Type<__bf16> {
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     }
+    // sixteen contraction indices, four a lane
+    static __device__ v4f mma16(v2i a, v2i b, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a), __builtin_bit_cast(s4, b), c, 0, 0, 0);
+    }
     static __device__ v4i pack(v4f a, v4f b) {
         return __builtin_bit_cast(v4i, bf8{(__bf16)a[0], (__bf16)a[1], (__bf16)a[2], (__bf16)a[3], (__bf16)b[0],
                                            (__bf16)b[1], (__bf16)b[2], (__bf16)b[3]});
@@ -44,6 +51,10 @@ struct Type<_Float16> {
     static constexpr unsigned kExp = 0x7c00u, kOne = 0x3c00u;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+    static __device__ v4f mma16(v2i a, v2i b, v4f c) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(h4, a), __builtin_bit_cast(h4, b), c, 0, 0, 0);
     }
     static __device__ v4i pack(v4f a, v4f b) {
         return __builtin_bit_cast(v4i, h8{(_Float16)a[0], (_Float16)a[1], (_Float16)a[2], (_Float16)a[3],
@@ -75,21 +86,19 @@ __device__ inline int lds_at(int r, int chunk) {
     return r * kRowBytes + ((chunk ^ swizzle<kRowBytes>(r)) << 4);
 }
 
-typedef short s4 __attribute__((ext_vector_type(4)));
-
 // The left operand of the second product: contraction step u (32 cache rows of a 16-bit tile, 16
 // of a 32-bit one) and output columns 16 dt .. 16 dt + 15.  Slot j = 4t + i of lane group g is cache
 // row 32u + 16t + 4g + i (t = 0 only for 32-bit).
-template <typename T, int D>
+// (kPairs false: 16 cache rows of a 16-bit tile, in the first two words.)
+template <typename T, int D, bool kPairs = true>
 __device__ inline v4i v_operand(const char *vt, int u, int dt, int lane) {
     constexpr int RB = D * sizeof(T);
     const int g = lane >> 4, n = lane & 15;
     if constexpr (sizeof(T) == 2) {
-        typedef int v2i __attribute__((ext_vector_type(2)));
-        v2i part[2];
+        v2i part[2] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int row = 32 * u + 16 * t + 4 * g + (n >> 2);
+        for (int t = 0; t < (kPairs ? 2 : 1); ++t) {
+            const int row = (kPairs ? 32 : 16) * u + 16 * t + 4 * g + (n >> 2);
             const char *p = vt + lds_at<RB>(row, 2 * dt + ((n & 3) >> 1)) + 8 * (n & 1);
             part[t] = __builtin_bit_cast(
                 v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
@@ -323,7 +332,6 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
         // ---- running maximum and sum; the sum keeps the weights unrounded.  The base of the exponentials follows
         // the maximum only when that has grown by more than 2^kSlack: weights up to 2^kSlack lose nothing (their
         // relative rounding is the same), and most tiles need no rescaling of o.
-        constexpr float kSlack = 6.f;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float mx = kNegInf;
@@ -504,11 +512,283 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
     }
 }
 
+// ---- few query rows (at most 16 per (lane, kv head): decode, short drafts with small groups)
+//
+// The cache is read once and the products are small: bound by bytes, or by latency where the cache is short.
+// Every wave takes whole tiles of its own, wave w the tiles w, w + 4, ... of the workgroup's part, and keeps
+// a running maximum, sum and output of its own for the 16 rows; the four are joined through LDS at the end.
+// So no wave waits for another in the loop.  K rows go from memory straight into operand registers (a lane
+// reads 16 bytes of row lane % 16); V rows, whose operand needs four rows of one column, through 8 KiB of LDS
+// that only this wave uses.  A tile is 8 KiB of K and of V, 64 registers; the next tile's loads are issued as soon
+// as K has gone into the products and V into LDS, and are in flight during the softmax and the second product.
+constexpr int kFewWaves = 4, kFewRows = 16;
+constexpr int few_tile(int row_bytes) { return 8192 / row_bytes; }
+
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int RB = D * sizeof(T), TOK = few_tile(RB), NT = TOK / 16, NS = RB / 64, ND = D / 16;
+    constexpr int TPR = RB / 16, RPP = 64 / TPR, NP = TOK / RPP;
+    constexpr bool kPairs = sizeof(T) == 2 && TOK >= 32;  // the second product in steps of 32 rows
+    constexpr int NU = kPairs ? TOK / 32 : NT;
+    constexpr int kBuf = 16 * D * 4 > 8192 ? 16 * D * 4 : 8192;  // a wave's V tile, at the end its output
+    constexpr unsigned long long kFull = TOK == 64 ? ~0ull : (1ull << TOK) - 1ull;
+    __shared__ __attribute__((aligned(16))) char s_buf[kFewWaves][kBuf];
+    __shared__ float s_m[kFewWaves][16], s_l[kFewWaves][16];
+
+    const AttnDims &d = a.d;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const bool tree = a.l.parents != nullptr;
+    const unsigned b = blockIdx.x;
+    const int split = b % plan.splits, ch = b / plan.splits, h = ch % d.Hkv, c = ch / d.Hkv;
+    const Lane ln = paged_lane(d, a.l, c);
+    if (ln.slot == -1) return;
+    int bits = ln.bits;
+    unsigned anc = 0;
+    if (tree && !(bits & GDN_STATUS_NODES)) {
+        bool bad;
+        anc = tree_ancestors(a.l.parents + (int64_t)c * d.N, ln.nodes, bad);
+        if (bad) bits |= GDN_STATUS_PARENT;
+    }
+    if (bits) {
+        if (a.l.status && split == 0 && h == 0 && tid == 0) atomicOr(a.l.status, bits);
+        return;
+    }
+    const int rows = ln.nodes * d.G, L = ln.len;
+    if (rows == 0) return;
+    const Reach rc = reach(tree, L, ln.nodes, ln.nodes - 1, plan.splits, TOK * kFewWaves);
+    const int t0 = split * rc.part, t1 = min(t0 + rc.part, rc.end);
+    if (t0 >= t1) return;
+
+    const int r = min(n, rows - 1), token = r / d.G;
+    const unsigned sees = __shfl(anc, token & 63);
+    const int64_t node = (int64_t)c * d.N + token;
+    const int head = h * d.G + r - token * d.G;
+    v4i qf[NS];
+    {
+        const char *q = reinterpret_cast<const char *>(static_cast<const T *>(a.q) + (node * d.Hq + head) * D);
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) qf[ks] = *reinterpret_cast<const v4i *>(q + 64 * ks + 16 * g);
+    }
+
+    // ---- cache rows of a tile: lane j finds row t + j
+    const int32_t *table = a.l.page_table + (int64_t)ln.slot * d.max_pages;
+    auto fetch = [&](int t) { return table[d.page((uint32_t)min(t + lane, t1 - 1))]; };
+    v4i kr[NT * NS], vr[NP];
+    auto load = [&](int t, int pid) {  // the tile's rows with a page, as a bit set; the others are loaded from row 0
+        const uint32_t tk = t + lane;
+        const bool ok = lane < TOK && (int)tk < t1 && (unsigned)pid < (unsigned)d.n_pages;
+        const uint32_t mine = ok ? cache_row(d, pid, h, tk, d.page(tk)) : 0u;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+            const size_t at = (size_t)(uint32_t)__shfl((int)mine, 16 * tt + n) * RB + 16 * g;
+#pragma unroll
+            for (int ks = 0; ks < NS; ++ks)
+                kr[tt * NS + ks] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at + 64 * ks);
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const size_t at = (size_t)(uint32_t)__shfl((int)mine, RPP * p + lane / TPR) * RB + 16 * (lane % TPR);
+            vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
+        }
+        return __builtin_amdgcn_ballot_w64(ok);
+    };
+
+    v4f o[ND];
+    float m = kNegInf, l = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) o[dt] = v4f{0.f, 0.f, 0.f, 0.f};
+    constexpr int kStep = TOK * kFewWaves;
+    char *s_v = s_buf[wave];
+
+    // The softmax and the second product of a tile whose scores are in s and whose V rows are in LDS.
+    v4f s[NT];
+    auto finish = [&](auto masked, int t, unsigned long long have) {
+        constexpr bool kMasked = decltype(masked)::value;
+        unsigned long long see = 0;
+        if constexpr (kMasked) {  // the tile's rows that this query row attends to
+            const int rel = L - t;
+            see = low_bits(tree ? rel : rel + token + 1);
+            if (tree) {
+                const unsigned long long nodes = sees;
+                see |= rel >= 64 || rel <= -32 ? 0 : rel >= 0 ? nodes << rel : nodes >> -rel;
+            }
+            see = (see & have) >> (4 * g);
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[tt][i] = (see >> (16 * tt + i)) & 1 ? s[tt][i] : kNegInf;
+        }
+        float mx = kNegInf;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[tt][i]);
+        mx = lane_max(mx) * a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack || (mx > m && m == kNegInf))) {
+            const float to = fmaxf(m, mx), base = to == kNegInf ? 0.f : to;
+            const float shrink = __builtin_amdgcn_exp2f(m - base);
+            m = to;
+            l *= shrink;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) o[dt] *= shrink;
+        }
+        const float base = m == kNegInf ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[tt][i] = __builtin_amdgcn_exp2f(fmaf(s[tt][i], a.scale_log2, -base));
+                sum += s[tt][i];
+            }
+        l += sum;
+        bool strange = false;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            v4i pf;
+            if constexpr (kPairs)
+                pf = Type<T>::pack(s[2 * u], s[2 * u + 1]);
+            else if constexpr (sizeof(T) == 2)
+                pf = Type<T>::pack(s[u], v4f{0.f, 0.f, 0.f, 0.f});
+            else
+                pf = __builtin_bit_cast(v4i, s[u]);
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) {
+                v4i vf = v_operand<T, D, kPairs>(s_v, u, dt, lane);
+                if constexpr (kMasked) strange |= drop_nonfinite<T>(vf);
+                if constexpr (kPairs || sizeof(T) == 4)
+                    o[dt] = Type<T>::mma(vf, pf, o[dt]);
+                else
+                    o[dt] = Type<T>::mma16(v2i{vf[0], vf[1]}, v2i{pf[0], pf[1]}, o[dt]);
+            }
+        }
+        if constexpr (kMasked)  // infinities and NaN go to the rows that attend to them, as in the row kernel
+            if (__builtin_amdgcn_ballot_w64(strange)) {
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {
+                    const float inf = side ? kNegInf : -kNegInf;
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) {
+                        v4f one[2];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            one[j >> 2][j & 3] = (kPairs || j < 4) && (see >> ((kPairs ? 32 * u + 16 * (j >> 2) : 16 * u) + (j & 3))) & 1 ? 1.f : 0.f;
+                        v4i reads;
+                        if constexpr (sizeof(T) == 2)
+                            reads = Type<T>::pack(one[0], one[1]);
+                        else
+                            reads = __builtin_bit_cast(v4i, one[0]);
+#pragma unroll
+                        for (int dt = 0; dt < ND; ++dt) {
+                            const v4i vf = nonfinite_ones<T>(v_operand<T, D, kPairs>(s_v, u, dt, lane), side);
+                            v4f cnt{0.f, 0.f, 0.f, 0.f};
+                            if constexpr (kPairs || sizeof(T) == 4)
+                                cnt = Type<T>::mma(vf, reads, cnt);
+                            else
+                                cnt = Type<T>::mma16(v2i{vf[0], vf[1]}, v2i{reads[0], reads[1]}, cnt);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[dt][i] += cnt[i] > 0.f ? inf : 0.f;
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                }
+            }
+    };
+
+    const int all_see = tree ? L : L + 1;  // rows in front of this: seen by every query row
+    int t = t0 + wave * TOK;
+    if (t < t1) {
+        unsigned long long have = load(t, fetch(t));
+        int pid = fetch(t + kStep);
+        for (; t < t1; t += kStep) {
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+                s[tt] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < NS; ++ks) s[tt] = Type<T>::mma(kr[tt * NS + ks], qf[ks], s[tt]);
+            }
+            const unsigned long long here = have;
+            if (here != kFull) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    const bool ok = (here >> (RPP * p + lane / TPR)) & 1;
+                    vr[p] = v4i{ok ? vr[p][0] : 0, ok ? vr[p][1] : 0, ok ? vr[p][2] : 0, ok ? vr[p][3] : 0};
+                }
+                if (lane == 0 && a.l.status && here != (kFull & low_bits(t1 - t))) atomicOr(a.l.status, GDN_STATUS_PAGE);
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                *reinterpret_cast<v4i *>(s_v + lds_at<RB>(RPP * p + lane / TPR, lane % TPR)) = vr[p];
+            if (t + kStep < t1) {
+                have = load(t + kStep, pid);
+                pid = fetch(t + 2 * kStep);
+            }
+            if (t + TOK > all_see || here != kFull)
+                finish(std::true_type{}, t, here);
+            else
+                finish(std::false_type{}, t, here);
+        }
+    }
+
+    // ---- the four waves' outputs joined: 4-column groups of a row at place (group ^ row)
+    l = lane_sum(l);
+    if (g == 0) {
+        s_m[wave][n] = m;
+        s_l[wave][n] = l;
+    }
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt)
+        *reinterpret_cast<v4f *>(s_v + (n * (D / 4) + ((4 * dt + g) ^ n)) * 16) = o[dt];
+    __syncthreads();
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq;
+    for (int k = tid; k < rows * (D / 4); k += 64 * kFewWaves) {
+        const int row = k / (D / 4), col = k % (D / 4);
+        float mx = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) mx = fmaxf(mx, s_m[w][row]);
+        v4f acc{0.f, 0.f, 0.f, 0.f};
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) {
+            const float mw = s_m[w][row], lw = s_l[w][row];
+            const float wgt = mw == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mw - mx);
+            const v4f v = *reinterpret_cast<const v4f *>(s_buf[w] + (row * (D / 4) + (col ^ row)) * 16);
+            if (wgt != 0.f) acc += v * wgt;
+            sum += lw == 0.f ? 0.f : lw * wgt;
+        }
+        if (plan.splits > 1) {
+            const size_t at = (size_t)split * all_rows + ((size_t)c * d.Hkv + h) * d.N * d.G + row;
+            *reinterpret_cast<v4f *>(a.workspace + at * D + 4 * col) = acc;
+            if (col == 0) {
+                float *ml = a.workspace + plan.splits * all_rows * D + at * 2;
+                ml[0] = mx;
+                ml[1] = sum;
+            }
+            continue;
+        }
+        const int tk = row / d.G, hd = h * d.G + row - tk * d.G;
+        const int64_t nd = (int64_t)c * d.N + tk;
+        v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : acc / sum;
+        if (a.gate.p) {
+            const v4f z = load4(static_cast<const T *>(a.gate.p) + nd * a.gate.token + hd * a.gate.head + 4 * col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = gated(v[i], z[i], a.gate_mode);
+        }
+        store4(static_cast<T *>(a.out) + (nd * d.Hq + hd) * D + 4 * col, v);
+    }
+}
+
+// Parts of the cache are whole tiles of the kernel that works on them.
+template <typename T, int D>
+__device__ inline int part_rows(int rows_per_group) {
+    return rows_per_group == kFewRows ? few_tile(D * sizeof(T)) * kFewWaves : tile_rows(D * sizeof(T));
+}
+
 constexpr int kJoinWaves = 4;
 // Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
-    constexpr int TOK = tile_rows(D * sizeof(T)), W = D / 64;
+    constexpr int W = D / 64;
     typedef float vw __attribute__((ext_vector_type(W)));
     typedef T tw __attribute__((ext_vector_type(W)));
     const AttnDims &d = a.d;
@@ -525,7 +805,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
         if (bad) return;
     }
     const int bm = plan.rows_per_group;
-    const Reach rc = reach(tree, ln.len, ln.nodes, (r / bm * bm + bm - 1) / d.G, plan.splits, TOK);
+    const Reach rc = reach(tree, ln.len, ln.nodes, (r / bm * bm + bm - 1) / d.G, plan.splits, part_rows<T, D>(bm));
     const int parts = (rc.end + rc.part - 1) / rc.part;
     const float *ml = a.workspace + plan.splits * all_rows * D + row * 2, *po = a.workspace + row * D + lane * W;
     const float mine = lane < parts ? ml[lane * all_rows * 2] : kNegInf;
@@ -570,7 +850,10 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     constexpr int RB = D * sizeof(T), kWaves = row_waves(RB);
     const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
     const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units), block(64 * kWaves);
-    if (p.rows_per_group == 16 * kWaves)
+    if (p.rows_per_group == kFewRows) {
+        if constexpr (RB < 1024)
+            hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
+    } else if (p.rows_per_group == 16 * kWaves)
         hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, block, 0, stream, a, p);
     else if constexpr (kWaves == 4)
         hipLaunchKernelGGL((attn_rows_kernel<T, D, 2>), grid, block, 0, stream, a, p);
@@ -593,12 +876,15 @@ hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
 
 AttnPlan attn_plan(const AttnDims &d) {
     AttnPlan p;
-    const int waves = row_waves(d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2));
-    p.rows_per_group = waves == 4 && (int64_t)d.N * d.G <= 64 ? 64 : 128;
-    p.tiles = (int)(((int64_t)d.N * d.G + p.rows_per_group - 1) / p.rows_per_group);
+    const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
+    const int64_t rows = (int64_t)d.N * d.G;
+    const bool few = rows <= kFewRows && row_bytes < 1024;
+    p.rows_per_group = few ? kFewRows : row_waves(row_bytes) == 4 && rows <= 64 ? 64 : 128;
+    p.tiles = (int)((rows + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
-    const int64_t most = ((int64_t)d.max_pages * d.page.d + 255) / 256;  // parts of at least 256 rows
-    int64_t s = groups >= 512 ? 1 : (1024 + groups - 1) / groups;
+    const int64_t least = few ? few_tile(row_bytes) * kFewWaves : 256;  // rows of a part
+    const int64_t most = ((int64_t)d.max_pages * d.page.d + least - 1) / least;
+    int64_t s = groups >= 512 ? 1 : ((few ? 1024 : 512) + groups - 1) / groups;
     if (s > most) s = most;
     p.splits = (int)(s > 64 ? 64 : s);
     return p;
