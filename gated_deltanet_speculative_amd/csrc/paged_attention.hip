@@ -186,6 +186,23 @@ __device__ inline v4f load4(const T *p) {
 }
 __device__ inline float gated(float o, float z, int mode) { return o * (mode == 0 ? fast_silu(z) : fast_sigmoid(z)); }
 
+// What a workgroup leaves for the join, one pair per (split, query row) behind the partial outputs: the running
+// maximum and sum; maximum -inf and sum 0 where the part holds nothing; a NaN maximum where the row is absent or its
+// lane is not computed, so that the join looks at nothing else of the lane.
+__device__ inline float *join_pairs(const AttnArgs &a, const AttnPlan &plan) {
+    return a.workspace + (size_t)plan.splits * a.d.C * a.d.N * a.d.Hq * a.d.D;
+}
+// The same pair for rows r0 .. r0 + n - 1 of a (lane, kv head), by the whole workgroup.
+__device__ inline void leave_nothing(const AttnArgs &a, const AttnPlan &plan, int split, int c, int h, int r0, int n, float mx) {
+    const AttnDims &d = a.d;
+    const int per = d.N * d.G;
+    float *p = join_pairs(a, plan) + 2 * ((size_t)split * d.C * d.N * d.Hq + ((size_t)c * d.Hkv + h) * per);
+    for (int r = r0 + (int)threadIdx.x; r < min(r0 + n, per); r += blockDim.x) {
+        p[2 * r] = mx;
+        p[2 * r + 1] = 0.f;
+    }
+}
+
 // Query rows split over the waves (16 RT each), cache tiles shared through LDS: each wave's products
 // read the tile once, so the LDS traffic per product falls with RT.  Two tiles of LDS, one barrier
 // per tile: the next tile's rows are loaded to registers while the current one is worked on (its page
@@ -212,10 +229,14 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
     const int split = b % plan.splits;
     // heavy row tiles of a chain (the last tokens) first
     const int tile = plan.tiles - 1 - (b / plan.splits) % plan.tiles;
-    const int ch = b / (plan.splits * plan.tiles), h = ch % d.Hkv, c = ch / d.Hkv;
+    const int ch = b / (plan.splits * plan.tiles), h = ch % d.Hkv, c = ch / d.Hkv, r0 = tile * BM;
+    const float skip = __builtin_nanf("");
 
     const Lane ln = paged_lane(d, a.l, c);
-    if (ln.slot == -1) return;
+    if (ln.slot == -1) {
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, r0, BM, skip);
+        return;
+    }
     int bits = ln.bits;
     unsigned anc = 0;
     if (tree && !(bits & GDN_STATUS_NODES)) {
@@ -225,13 +246,18 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
     }
     if (bits) {
         if (a.l.status && split == 0 && tile == 0 && h == 0 && tid == 0) atomicOr(a.l.status, bits);
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, r0, BM, skip);
         return;
     }
-    const int rows = ln.nodes * d.G, r0 = tile * BM, L = ln.len;
+    const int rows = ln.nodes * d.G, L = ln.len;
+    if (plan.splits > 1 && rows < r0 + BM) leave_nothing(a, plan, split, c, h, max(r0, rows), BM, skip);
     if (r0 >= rows) return;
     const Reach rc = reach(tree, L, ln.nodes, (r0 + BM - 1) / d.G, plan.splits, TOK);
     const int t0 = split * rc.part, t1 = min(t0 + rc.part, rc.end);
-    if (t0 >= t1) return;
+    if (t0 >= t1) {  // (only with several splits)
+        leave_nothing(a, plan, split, c, h, r0, min(BM, rows - r0), kNegInf);
+        return;
+    }
 
     // ---- this wave's query rows (zeros behind the last one) and what they attend to
     const int rw = r0 + wave * 16 * RT;
@@ -488,7 +514,7 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) *reinterpret_cast<v4f *>(po + 16 * dt + 4 * g) = o[rt][dt];
             if (g == 0) {
-                float *ml = a.workspace + plan.splits * all_rows * D + row * 2;
+                float *ml = join_pairs(a, plan) + row * 2;
                 ml[0] = m[rt];
                 ml[1] = sum;
             }
@@ -540,8 +566,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
     const bool tree = a.l.parents != nullptr;
     const unsigned b = blockIdx.x;
     const int split = b % plan.splits, ch = b / plan.splits, h = ch % d.Hkv, c = ch / d.Hkv;
+    const float skip = __builtin_nanf("");
     const Lane ln = paged_lane(d, a.l, c);
-    if (ln.slot == -1) return;
+    if (ln.slot == -1) {
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, 0, kFewRows, skip);
+        return;
+    }
     int bits = ln.bits;
     unsigned anc = 0;
     if (tree && !(bits & GDN_STATUS_NODES)) {
@@ -551,13 +581,18 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
     }
     if (bits) {
         if (a.l.status && split == 0 && h == 0 && tid == 0) atomicOr(a.l.status, bits);
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, 0, kFewRows, skip);
         return;
     }
     const int rows = ln.nodes * d.G, L = ln.len;
+    if (plan.splits > 1) leave_nothing(a, plan, split, c, h, rows, kFewRows, skip);
     if (rows == 0) return;
     const Reach rc = reach(tree, L, ln.nodes, ln.nodes - 1, plan.splits, TOK * kFewWaves);
     const int t0 = split * rc.part, t1 = min(t0 + rc.part, rc.end);
-    if (t0 >= t1) return;
+    if (t0 >= t1) {  // (only with several splits)
+        leave_nothing(a, plan, split, c, h, 0, rows, kNegInf);
+        return;
+    }
 
     const int r = min(n, rows - 1), token = r / d.G;
     const unsigned sees = __shfl(anc, token & 63);
@@ -760,7 +795,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
             const size_t at = (size_t)split * all_rows + ((size_t)c * d.Hkv + h) * d.N * d.G + row;
             *reinterpret_cast<v4f *>(a.workspace + at * D + 4 * col) = acc;
             if (col == 0) {
-                float *ml = a.workspace + plan.splits * all_rows * D + at * 2;
+                float *ml = join_pairs(a, plan) + at * 2;
                 ml[0] = mx;
                 ml[1] = sum;
             }
@@ -778,38 +813,29 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
     }
 }
 
-// Parts of the cache are whole tiles of the kernel that works on them.
-template <typename T, int D>
-__device__ inline int part_rows(int rows_per_group) {
-    return rows_per_group == kFewRows ? few_tile(D * sizeof(T)) * kFewWaves : tile_rows(D * sizeof(T));
-}
-
 constexpr int kJoinWaves = 4;
-// Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.
+// Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.  What there is to
+// join stands beside the parts (join_pairs), so that no read waits for another but the first.
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
-    constexpr int W = D / 64;
+    constexpr int W = D / 64, kAhead = 8;  // parts loaded together
     typedef float vw __attribute__((ext_vector_type(W)));
     typedef T tw __attribute__((ext_vector_type(W)));
     const AttnDims &d = a.d;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, parts = plan.splits;
     const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
     if (row >= all_rows) return;
-    const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
-    const bool tree = a.l.parents != nullptr;
-    const Lane ln = paged_lane(d, a.l, c);
-    if (ln.slot == -1 || ln.bits || r >= ln.nodes * d.G) return;
-    if (tree) {
-        bool bad;
-        tree_ancestors(a.l.parents + (int64_t)c * d.N, ln.nodes, bad);
-        if (bad) return;
-    }
-    const int bm = plan.rows_per_group;
-    const Reach rc = reach(tree, ln.len, ln.nodes, (r / bm * bm + bm - 1) / d.G, plan.splits, part_rows<T, D>(bm));
-    const int parts = (rc.end + rc.part - 1) / rc.part;
-    const float *ml = a.workspace + plan.splits * all_rows * D + row * 2, *po = a.workspace + row * D + lane * W;
-    const float mine = lane < parts ? ml[lane * all_rows * 2] : kNegInf;
-    const float part_sum = lane < parts ? ml[lane * all_rows * 2 + 1] : 0.f;
+    const float *ml = join_pairs(a, plan) + row * 2, *po = a.workspace + row * D + lane * W;
+    vw v[kAhead];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            v[j] = *reinterpret_cast<const vw *>(po + (size_t)min(p0 + j, parts - 1) * all_rows * D);
+    };
+    load(0);
+    const float mine = ml[(size_t)min(lane, parts - 1) * all_rows * 2];
+    const float part_sum = lane < parts ? ml[(size_t)lane * all_rows * 2 + 1] : 0.f;
+    if (__builtin_amdgcn_ballot_w64(mine != mine)) return;  // an absent row
     float mx = mine;
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
@@ -819,18 +845,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
     vw acc = 0.f;
-    constexpr int kAhead = 8;  // parts loaded together
     for (int p0 = 0; p0 < parts; p0 += kAhead) {
-        vw v[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            v[j] = *reinterpret_cast<const vw *>(po + (size_t)min(p0 + j, parts - 1) * all_rows * D);
+        if (p0) load(p0);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const float w = p0 + j < parts ? __shfl(wgt, p0 + j) : 0.f;
             if (w != 0.f) acc += v[j] * w;
         }
     }
+    const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
     const int token = r / d.G, head = h * d.G + r - token * d.G;
     const int64_t node = (int64_t)c * d.N + token;
     acc = sum == 0.f ? vw(0.f) : acc / sum;
@@ -882,9 +905,12 @@ AttnPlan attn_plan(const AttnDims &d) {
     p.rows_per_group = few ? kFewRows : row_waves(row_bytes) == 4 && rows <= 64 ? 64 : 128;
     p.tiles = (int)((rows + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
-    const int64_t least = few ? few_tile(row_bytes) * kFewWaves : 256;  // rows of a part
+    const int64_t least = few ? few_tile(row_bytes) * kFewWaves : 256;  // cache rows of a part
     const int64_t most = ((int64_t)d.max_pages * d.page.d + least - 1) / least;
-    int64_t s = groups >= 512 ? 1 : ((few ? 1024 : 512) + groups - 1) / groups;
+    // one round of workgroups: two of them fit a CU (more of them, shorter: tree of 4x16 at 8k 43 us with 512, 52 with
+    // 1024; decode of 64 lanes 592 and 581; 5x8 float32 chains at 3k 21.7 and 24.8)
+    constexpr int64_t kRound = 512;
+    int64_t s = (kRound + groups - 1) / groups;
     if (s > most) s = most;
     p.splits = (int)(s > 64 ? 64 : s);
     return p;
