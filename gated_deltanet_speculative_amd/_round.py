@@ -8,6 +8,7 @@ stream passed on.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple, Optional
 
@@ -106,6 +107,8 @@ def _library():
 
 
 # ---------------------------------------------------------------- marshalling helpers
+# A small call is bound by this file: a tensor costs about half a microsecond here, so the checks ask for
+# what is cheap to ask for (the device as its index) and leave finding the message to _refuse.
 def _refuse(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -113,17 +116,17 @@ def _refuse(t, name, dtype, shape, device):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
+    if t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, the call's first tensor on cuda:{device}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _ptr(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
+def _ptr(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
     """Pointer of a contiguous tensor of this type and shape on this device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
-            and t.is_cuda and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
         _refuse(t, name, dtype, shape, device)
     return t.data_ptr()
 
@@ -132,20 +135,20 @@ def _opt(t, name, dtype, shape, device) -> Optional[int]:
     return None if t is None else _ptr(t, name, dtype, shape, device)
 
 
-def _device(t, name) -> torch.device:
+def _device(t, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.device
+    return t.get_device()
 
 
-def _view(t, name: str, dtype: torch.dtype, sh: AttnShape, heads: int, device: torch.device) -> _CView:
+def _view(t, name: str, dtype: torch.dtype, sh: AttnShape, heads: int, device: int) -> _CView:
     """A [C, N, heads, D] tensor whose last dimension is contiguous and whose tokens are evenly
     strided over the lanes (a slice of a stacked projection, or a contiguous tensor)."""
-    C, N, D = sh.n_seqs, sh.n_nodes, sh.head_dim
-    shape = (C, N, heads, D)
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda):
+    C, N = sh.n_seqs, sh.n_nodes
+    shape = (C, N, heads, sh.head_dim)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device):
         _refuse(t, name, dtype, shape, device)
     s0, s1, s2, s3 = t.stride()
     if s3 != 1:
@@ -163,19 +166,22 @@ def _status_word(status, device) -> torch.Tensor:
     return status
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _call(device, f, name, *args) -> None:
-    """Calls f with the tensors' device current: a launch goes to the stream's device."""
-    if torch.cuda.current_device() == device.index:
-        code = f(*args)
+def _call(device: int, f, name, *args) -> None:
+    """f(*args, stream) with torch's current stream of the tensors' device, which is made current: a launch
+    goes to the stream's device."""
+    if torch._C._cuda_getDevice() == device:
+        code = f(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            code = f(*args)
+            code = f(*args, torch._C._cuda_getCurrentRawStream(device))
     if code != GDN_OK:
         raise GdnError(code, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _cs(sh):
+    """The C struct of a shape (never written to)."""
+    return sh.c_struct()
 
 
 def _places(sh: AttnShape, slot_ids, page_table, seq_len, device) -> tuple:
@@ -214,7 +220,7 @@ def rope_kv_write(sh: AttnShape, q, k, v, inv_freq, k_cache, v_cache, slot_ids, 
     if q_out is None:
         q_out = torch.empty((C, N, sh.n_q_heads, D), dtype=sh.dtype, device=device)
     status = _status_word(status, device)
-    x = q.dtype if q.dtype == torch.float32 else sh.dtype
+    x = torch.float32 if q.dtype is torch.float32 else sh.dtype
     views = [_view(t, n, x, sh, heads, device) for t, n, heads in
              ((q, "q", sh.n_q_heads), (k, "k", sh.n_kv_heads), (v, "v", sh.n_kv_heads))]
     rope = _CRope(_ptr(inv_freq, "inv_freq", torch.float64, (half,), device),
@@ -222,17 +228,17 @@ def rope_kv_write(sh: AttnShape, q, k, v, inv_freq, k_cache, v_cache, slot_ids, 
                   _opt(pair_axis, "pair_axis", torch.int32, (half,), device), n_axes, 2 * half, int(bool(interleaved)),
                   _opt(q_norm, "q_norm", torch.float32, (D,), device),
                   _opt(k_norm, "k_norm", torch.float32, (D,), device), eps)
-    _call(device, _library().gdn_rope_kv_write, "gdn_rope_kv_write", ctypes.byref(sh.c_struct()), _dtype_code(x),
+    _call(device, _library().gdn_rope_kv_write, "gdn_rope_kv_write", ctypes.byref(_cs(sh)), _dtype_code(x),
           *map(ctypes.byref, views), ctypes.byref(rope), _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
           _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *_places(sh, slot_ids, page_table, seq_len, device),
           *_tree(sh, parents, lane_nodes, device),
-          _ptr(q_out, "q_out", sh.dtype, (C, N, sh.n_q_heads, D), device), status.data_ptr(), _stream(device))
+          _ptr(q_out, "q_out", sh.dtype, (C, N, sh.n_q_heads, D), device), status.data_ptr())
     return q_out, status
 
 
 def paged_attention_workspace_size(sh: AttnShape) -> int:
     """Bytes of device workspace paged_attention needs for this shape (0 for an invalid shape)."""
-    return int(_library().gdn_paged_attention_workspace_size(ctypes.byref(sh.c_struct())))
+    return int(_library().gdn_paged_attention_workspace_size(ctypes.byref(_cs(sh))))
 
 
 def paged_attention(sh: AttnShape, q, k_cache, v_cache, slot_ids, page_table, seq_len, parents=None, lane_nodes=None,
@@ -247,7 +253,7 @@ def paged_attention(sh: AttnShape, q, k_cache, v_cache, slot_ids, page_table, se
     if out is None:
         out = torch.empty(shape, dtype=sh.dtype, device=device)
     status = _status_word(status, device)
-    lib, cs = _library(), ctypes.byref(sh.c_struct())
+    lib, cs = _library(), ctypes.byref(_cs(sh))
     if workspace is None:
         workspace = torch.empty(max(lib.gdn_paged_attention_workspace_size(cs) // 4, 1), dtype=torch.float32, device=device)
     else:
@@ -257,13 +263,12 @@ def paged_attention(sh: AttnShape, q, k_cache, v_cache, slot_ids, page_table, se
           _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *_places(sh, slot_ids, page_table, seq_len, device),
           *_tree(sh, parents, lane_nodes, device), 1.0 / math.sqrt(sh.head_dim) if scale is None else scale,
           None if gate is None else ctypes.byref(_view(gate, "gate", sh.dtype, sh, sh.n_q_heads, device)), int(gate_mode),
-          _ptr(out, "out", sh.dtype, shape, device), workspace.data_ptr(), workspace.numel() * 4, status.data_ptr(),
-          _stream(device))
+          _ptr(out, "out", sh.dtype, shape, device), workspace.data_ptr(), workspace.numel() * 4, status.data_ptr())
     return out, status
 
 
 def _scratch(workspace, device) -> torch.Tensor:
-    if not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32 and workspace.device == device
+    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.float32 and workspace.get_device() == device
             and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous float32 tensor on the call's device")
     return workspace
@@ -271,7 +276,7 @@ def _scratch(workspace, device) -> torch.Tensor:
 
 def draft_accept_workspace_size(sh: AcceptShape) -> int:
     """Bytes of device workspace draft_accept needs for this shape (0 for an invalid shape)."""
-    return int(_library().gdn_draft_accept_workspace_size(ctypes.byref(sh.c_struct())))
+    return int(_library().gdn_draft_accept_workspace_size(ctypes.byref(_cs(sh))))
 
 
 def draft_accept(sh: AcceptShape, target, tokens, root_target=None, draft=None, parents=None, lane_nodes=None,
@@ -291,7 +296,7 @@ def draft_accept(sh: AcceptShape, target, tokens, root_target=None, draft=None, 
         _ptr(t, name, torch.int32, (C,), device)
         outs.append(t)
     status = _status_word(status, device)
-    lib, cs = _library(), ctypes.byref(sh.c_struct())
+    lib, cs = _library(), ctypes.byref(_cs(sh))
     if workspace is None:
         workspace = torch.empty(max(lib.gdn_draft_accept_workspace_size(cs) // 4, 1), dtype=torch.float32, device=device)
     else:
@@ -301,7 +306,7 @@ def draft_accept(sh: AcceptShape, target, tokens, root_target=None, draft=None, 
           _ptr(tokens, "tokens", torch.int32, (C, N), device), *_tree(sh, parents, lane_nodes, device),
           _opt(slot_ids, "slot_ids", torch.int32, (C,), device), _opt(u_accept, "u_accept", torch.float32, (C, N), device),
           _opt(u_next, "u_next", torch.float32, (C,), device), *(t.data_ptr() for t in outs), workspace.data_ptr(),
-          workspace.numel() * 4, status.data_ptr(), _stream(device))
+          workspace.numel() * 4, status.data_ptr())
     return (*outs, status)
 
 
@@ -330,9 +335,9 @@ def kv_commit_layers(sh: AttnShape, k_caches, v_caches, slot_ids, page_table, se
     if not 1 <= len(ks) <= MAX_LAYERS:
         raise ValueError(f"kv_commit_layers: {len(ks)} layers, expected 1..{MAX_LAYERS}")
     arr = _vp * len(ks)
-    _call(device, _library().gdn_kv_commit_layers, "gdn_kv_commit_layers", ctypes.byref(sh.c_struct()), len(ks), arr(*ks),
+    _call(device, _library().gdn_kv_commit_layers, "gdn_kv_commit_layers", ctypes.byref(_cs(sh)), len(ks), arr(*ks),
           arr(*vs), *_places(sh, slot_ids, page_table, seq_len, device), *_tree(sh, parents, lane_nodes, device),
           _ptr(accept_node, "accept_node", torch.int32, (sh.n_seqs,), device),
           _ptr(new_len, "new_len", torch.int32, (sh.n_slots,), device),
-          _ptr(status, "status", torch.int32, (1,), device), _stream(device))
+          _ptr(status, "status", torch.int32, (1,), device))
     return new_len
