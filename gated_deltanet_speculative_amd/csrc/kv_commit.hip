@@ -7,8 +7,9 @@
 // in place.  Each thread owns a 16-byte column of every row of one (lane, layer, K or V) and
 // kv head: no other thread reads or writes it, so the order within the thread is enough.
 //
-// Bound by launch and by the dependent reads of the preflight (slot, length, page id) in front of
-// the copies: every workgroup checks all lanes itself, as in the replay commit, so one launch decides.
+// Bound by launch and by dependent reads (slot, length, page id, row): every workgroup checks all lanes itself, as
+// in the replay commit, so one launch decides; its own rows are found and the first of them loaded ahead of the
+// verdict, and the preflight's entries are requested kBatch at a time.
 #include "round_device.h"
 
 namespace gdn {
@@ -16,40 +17,88 @@ namespace {
 
 constexpr int kThreads = 256;
 
+constexpr int kBatch = 8;  // preflight entries of a thread that are requested together
+constexpr int kAhead = 4;  // moved rows of a thread in flight
+
 __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers, CacheLayers cl, PagedLanes l,
                                                              const int32_t *__restrict__ accept_node,
                                                              int32_t *__restrict__ new_len, int row_chunks) {
     __shared__ unsigned s_bitmap[kBitmapSlots / 32];
     __shared__ int s_word, s_bits;
-    __shared__ uint32_t s_src[GDN_MAX_NODES], s_dst[GDN_MAX_NODES];  // cache rows of kv head 0
+    __shared__ int s_slot[GDN_MAX_SEQS], s_len[GDN_MAX_SEQS], s_nodes[GDN_MAX_SEQS];  // slot -1: padding or in error
+    __shared__ uint32_t s_src[GDN_MAX_NODES], s_dst[GDN_MAX_NODES];                   // cache rows of kv head 0
     const int tid = threadIdx.x, lane = tid & 63, c = blockIdx.y, side = blockIdx.x;
     const bool lengths = side == 2 * n_layers;  // the last workgroup of lane 0 writes the lengths
     if (lengths && c != 0) return;
 
-    // ---- preflight over every lane
+    // ---- this lane's path, rows and first loads, ahead of the verdict (a bad page is read as page 0)
     const int st_in = *l.status;
-    if (tid == 0) s_bits = 0;
     const LaneSlotsT<kThreads> slots(l.slot_ids, d.C);
+    const int e = accept_node[c];
+    int n = 0, first = 0;
+    unsigned path = 0;
+    const Lane own = paged_lane(d, l, c);
+    if (l.parents && !lengths && own.slot != -1 && !own.bits && e >= 0 && e < own.nodes) {
+        bool bad;
+        path = __shfl(tree_ancestors(l.parents + (int64_t)c * d.N, e + 1, bad), e);
+        n = __popc(path);
+        first = __builtin_ctz(~path);  // rows in front of the first gap stay (32: the whole path)
+        if (path == ~0u) first = 32;
+        if (tid < n) {
+            unsigned p = path;  // node a_tid: the tid-th set bit
+            for (int j = 0; j < tid; ++j) p &= p - 1u;
+            const uint32_t src = own.len + __builtin_ctz(p), dst = own.len + tid;
+            const int32_t *table = l.page_table + (int64_t)own.slot * d.max_pages;
+            const int ps = table[d.page(src)], pd = table[d.page(dst)];
+            s_src[tid] = (unsigned)ps < (unsigned)d.n_pages ? cache_row(d, ps, 0, src, d.page(src)) : 0u;
+            s_dst[tid] = (unsigned)pd < (unsigned)d.n_pages ? cache_row(d, pd, 0, dst, d.page(dst)) : 0u;
+        }
+    }
+    if (tid == 0) s_bits = 0;
+    lds_barrier();
+    v4i *cache = static_cast<v4i *>(lengths ? nullptr : side < n_layers ? cl.k[side] : cl.v[side - n_layers]);
+    const size_t head = (size_t)d.page.d * row_chunks;  // 16-byte chunks between the heads of a page
+    const int cols = d.Hkv * row_chunks;
+    v4i v[kAhead];
+    auto load = [&](int col, int j0) {
+        const v4i *p = cache + (col / row_chunks) * head + col % row_chunks;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (j0 + j < n) v[j] = p[(size_t)s_src[j0 + j] * row_chunks];
+    };
+    if (first < n && tid < cols) load(tid, first);
+
+    // ---- preflight over every lane
     int bits = slot_preflight<kThreads>(slots, l.slot_ids, d.C, d.P, s_bitmap, &s_word);  // (has barriers)
     for (int t = tid; t < d.C; t += kThreads) {
         const Lane ln = paged_lane(d, l, t);
-        if (ln.slot == -1) continue;
+        const int et = accept_node[t];
         bits |= ln.bits;
-        const int e = accept_node[t];
-        if (e < -1 || e >= min(max(ln.nodes, 0), d.N)) bits |= GDN_STATUS_ACCEPT;
+        if (ln.slot != -1 && (et < -1 || et >= min(max(ln.nodes, 0), d.N))) bits |= GDN_STATUS_ACCEPT;
+        s_slot[t] = ln.bits ? -1 : ln.slot;
+        s_len[t] = ln.len;
+        s_nodes[t] = ln.nodes;
     }
-    if (l.parents)
-        for (int k = tid; k < d.C * d.N; k += kThreads) {
-            const int t = k / d.N, i = k - t * d.N;
-            const Lane ln = paged_lane(d, l, t);
-            if (ln.slot == -1 || ln.bits || i >= ln.nodes) continue;
-            const int par = l.parents[k];
-            if (par < -1 || par >= i) bits |= GDN_STATUS_PARENT;
-            const int pid = l.page_table[(int64_t)ln.slot * d.max_pages + d.page((uint32_t)(ln.len + i))];
-            if ((unsigned)pid >= (unsigned)d.n_pages) bits |= GDN_STATUS_PAGE;
+    if (l.parents) {
+        lds_barrier();
+        for (int k0 = tid; k0 < d.C * d.N; k0 += kThreads * kBatch) {
+            int par[kBatch], pid[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) par[j] = l.parents[min(k0 + j * kThreads, d.C * d.N - 1)];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int k = min(k0 + j * kThreads, d.C * d.N - 1), t = k / d.N, i = k - t * d.N;
+                const bool has = s_slot[t] != -1 && i < s_nodes[t];
+                pid[j] = has ? l.page_table[(int64_t)s_slot[t] * d.max_pages + d.page((uint32_t)(s_len[t] + i))] : 0;
+                if (has && (par[j] < -1 || par[j] >= i)) bits |= GDN_STATUS_PARENT;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if ((unsigned)pid[j] >= (unsigned)d.n_pages) bits |= GDN_STATUS_PAGE;
         }
+    }
     if (bits) atomicOr(&s_bits, bits);
-    __syncthreads();
+    lds_barrier();
     bits = s_bits;
     const bool commit = st_in == 0 && bits == 0;
     if (bits && tid == 0 && side == 0) atomicOr(l.status, bits);
@@ -58,50 +107,27 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
         for (int s = tid; s < d.P; s += kThreads) new_len[s] = l.seq_len[s];
         if (!commit) return;
         __syncthreads();  // (the same addresses are written again below)
-        __threadfence_block();
         for (int t0 = 0; t0 < d.C; t0 += kThreads / 64) {  // a wave per lane
             const int t = t0 + (tid >> 6);
             if (t >= d.C) continue;
-            const int s = l.slot_ids[t], e = accept_node[t];
-            if (s == -1 || e < 0) continue;
-            int n = e + 1;
+            const int s = s_slot[t], et = accept_node[t];
+            if (s == -1 || et < 0) continue;
+            int m = et + 1;
             if (l.parents) {
                 bool bad;
-                const unsigned anc = tree_ancestors(l.parents + (int64_t)t * d.N, min(e + 1, d.N), bad);
-                n = __popc(__shfl(anc, e));
+                m = __popc(__shfl(tree_ancestors(l.parents + (int64_t)t * d.N, et + 1, bad), et));
             }
-            if (lane == 0) new_len[s] = l.seq_len[s] + n;
+            if (lane == 0) new_len[s] = s_len[t] + m;
         }
         return;
     }
+    if (!commit) return;
 
-    const int e = accept_node[c];
-    const Lane ln = paged_lane(d, l, c);
-    if (!commit || ln.slot == -1 || e < 0 || !l.parents) return;
-    bool bad;
-    const unsigned path = __shfl(tree_ancestors(l.parents + (int64_t)c * d.N, e + 1, bad), e);
-    const int n = __popc(path);
-    if (path == (n == 32 ? ~0u : (1u << n) - 1u)) return;  // the first n nodes: every row is in its place
-    if (tid < n) {
-        unsigned p = path;  // node a_tid: the tid-th set bit
-        for (int j = 0; j < tid; ++j) p &= p - 1u;
-        const uint32_t src = ln.len + __builtin_ctz(p), dst = ln.len + tid;
-        const int32_t *table = l.page_table + (int64_t)ln.slot * d.max_pages;
-        s_src[tid] = cache_row(d, table[d.page(src)], 0, src, d.page(src));
-        s_dst[tid] = cache_row(d, table[d.page(dst)], 0, dst, d.page(dst));
-    }
-    __syncthreads();
-    v4i *cache = static_cast<v4i *>(side < n_layers ? cl.k[side] : cl.v[side - n_layers]);
-    const size_t head = (size_t)d.page.d * row_chunks;  // 16-byte chunks between the heads of a page
-    const int first = __builtin_ctz(~path);             // rows in front of the first gap stay
-    for (int col = tid; col < d.Hkv * row_chunks; col += kThreads) {
+    // ---- the rows behind the first gap, kAhead loads in flight; a row written by a step is read by none behind it
+    for (int col = tid; col < cols; col += kThreads) {
         v4i *p = cache + (col / row_chunks) * head + col % row_chunks;
-        constexpr int kAhead = 4;  // loads in flight; a row written by these steps is read by none behind them
         for (int j0 = first; j0 < n; j0 += kAhead) {
-            v4i v[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (j0 + j < n) v[j] = p[(size_t)s_src[j0 + j] * row_chunks];
+            if (col != tid || j0 != first) load(col, j0);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
                 if (j0 + j < n) p[(size_t)s_dst[j0 + j] * row_chunks] = v[j];

@@ -92,12 +92,12 @@ struct AcceptArgs {
     void *workspace;
     int32_t *status;
 };
-constexpr int kAcceptChunk = 4096;  // vocabulary entries of one workgroup
+constexpr int kAcceptChunk = 1024;  // vocabulary entries of one wave of the sampled form
 __host__ __device__ inline int accept_chunks(int V) { return (V + kAcceptChunk - 1) / kAcceptChunk; }
 // Sampling keeps two 64-bit sums per (lane, chunk) and 16 bytes per lane; greedy a (value, index)
-// pair per (row, chunk).
+// pair per (row, 4096 values).
 inline size_t accept_workspace_bytes(int C, int N, int V) {
-    const size_t pairs = (size_t)C * (N + 1) * accept_chunks(V) * 8, sums = (size_t)C * (accept_chunks(V) + 1) * 16;
+    const size_t pairs = (size_t)C * (N + 1) * ((V + 4095) / 4096) * 8, sums = (size_t)C * (accept_chunks(V) + 1) * 16;
     return ((pairs > sums ? pairs : sums) + 15) / 16 * 16;
 }
 hipError_t launch_draft_accept(const AcceptArgs &a, hipStream_t stream);
