@@ -69,17 +69,19 @@ struct Type<float> {
 
 // Cache rows of a tile: 16 KiB of K and as much of V, at most 64 rows (a set of them is 64 bits).
 constexpr int tile_rows(int row_bytes) { return row_bytes < 256 ? 64 : 16384 / row_bytes; }
-// Waves of a workgroup of the row kernel.  Rows of 512 bytes and more leave a wave room for one tile of 16
-// query rows only (its outputs and queries alone are 96 registers and more): eight waves share a tile then,
-// so that the tile's loads and staging registers are shared by as many query rows.
-constexpr int row_waves(int row_bytes) { return row_bytes >= 512 ? 8 : 4; }
+// A workgroup of the row kernel: its waves, and tiles of 16 query rows per wave, by its query rows.  Two tiles per wave
+// halve the LDS reads per product; rows of 512 bytes and more leave room for one (its outputs and queries alone are
+// 96 registers and more).  Eight waves share a tile's loads and staging registers.
+constexpr int group_waves(int rows) { return rows == 64 ? 4 : 8; }
+constexpr int group_tiles(int rows) { return rows == 256 ? 2 : 1; }
 
 // A tile row of D values in LDS is D * sizeof(T) / 16 chunks of 16 bytes; chunk c of row r is kept
-// at place c ^ swizzle(r), so that the 16 rows (or 4 rows of each lane group) that one operand
-// read touches at the same column use distinct banks.
+// at place c ^ swizzle(r).  Eight lanes that read one column of eight rows (the first product) and sixteen that
+// read a 32-byte piece of four rows each (the second) then use distinct banks; the latter need the rows' pieces
+// two chunks apart (with r & 15 instead, rows 2k and 2k + 1 shared theirs: V reads took twice as long).
 template <int kRowBytes>
 __device__ inline int swizzle(int r) {
-    return kRowBytes == 128 ? (r >> 1) & 7 : r & 15;
+    return kRowBytes == 128 ? ((r >> 1) & 3) << 1 : (r & 7) << 1;
 }
 template <int kRowBytes>
 __device__ inline int lds_at(int r, int chunk) {
@@ -207,11 +209,12 @@ __device__ inline void leave_nothing(const AttnArgs &a, const AttnPlan &plan, in
 // read the tile once, so the LDS traffic per product falls with RT.  Two tiles of LDS, one barrier
 // per tile: the next tile's rows are loaded to registers while the current one is worked on (its page
 // ids a tile earlier) and written to the other half before the barrier.
-template <typename T, int D, int RT>
-__global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
-    constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = row_waves(RB), kThreads = 64 * kWaves, NT = TOK / 16, NS = RB / 64, ND = D / 16;
+template <typename T, int D, int BM>
+__global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = group_waves(BM), kThreads = 64 * kWaves, RT = group_tiles(BM), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
-    constexpr int BM = 16 * RT * kWaves, NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
+    static_assert(BM == 16 * RT * kWaves && RPP <= TOK, "");
+    constexpr int NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
     __shared__ __attribute__((aligned(16))) char s_kv[2][2][TOK * RB];
     // cache rows of a tile that lie in no page of the pool: by tile number mod 3 (written before the
     // tile's barrier, read behind it, cleared before the barrier of the second tile after it)
@@ -289,8 +292,7 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int tk = t + row_in + RPP * p;
-            pid[p] = table[d.page((uint32_t)min(tk, t1 - 1))];
-            pid[p] = tk < t1 ? pid[p] : -1;
+            pid[p] = table[d.page((uint32_t)min(tk, t1 - 1))];  // (not looked at before the load: nothing waits for it here)
         }
     };
     // (a row without a page is loaded from the pool's first row and cleared before it is used)
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const uint32_t tk = t + row_in + RPP * p;
-            const bool ok = (unsigned)pid[p] < (unsigned)d.n_pages;
+            const bool ok = (int)tk < t1 & (unsigned)pid[p] < (unsigned)d.n_pages;
             const uint32_t row = ok ? cache_row(d, pid[p], h, tk, d.page(tk)) : 0u;
             unpaged |= ok ? 0u : 1u << p;
             const size_t at = (size_t)row * RB + chunk * 16;
@@ -318,21 +320,26 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
+    constexpr int kMatrix = 0x8, kDsRead = 0x100, kMmaSteps = sizeof(T) == 2 ? 1 : 4;  // scheduling groups
     // One tile for this wave.  `masked`: some row does not attend to some of it.
     auto work = [&](auto masked, const char *s_k, const char *s_v, int t, unsigned long long gone) {
         constexpr bool kMasked = decltype(masked)::value;
         // ---- S^T = K Q^T
         v4f s[RT][NT];
 #pragma unroll
-        for (int tt = 0; tt < NT; ++tt) {
+        for (int ks = 0; ks < NS; ++ks)  // (outermost: the products of one tile depend on each other)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) s[rt][tt] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < NS; ++ks) {
+            for (int tt = 0; tt < NT; ++tt) {
                 const v4i kf = *reinterpret_cast<const v4i *>(s_k + lds_at<RB>(16 * tt + (lane & 15), 4 * ks + g));
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) s[rt][tt] = Type<T>::mma(kf, qf[rt][ks], s[rt][tt]);
+                for (int rt = 0; rt < RT; ++rt) s[rt][tt] = Type<T>::mma(kf, qf[rt][ks], ks ? s[rt][tt] : v4f{0.f, 0.f, 0.f, 0.f});
             }
+        // operand reads two steps ahead of their products
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * NT, 0);
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) {
+            __builtin_amdgcn_sched_group_barrier(kMatrix, NT * RT * kMmaSteps, 0);
+            __builtin_amdgcn_sched_group_barrier(kDsRead, NT, 0);
         }
         // ---- rows that are not attended weigh nothing, whatever their scores are: the tile's rows that a query
         // row attends to as a bit set, shifted so that this lane's rows are bits 16 tt + i
@@ -358,22 +365,31 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
         // ---- running maximum and sum; the sum keeps the weights unrounded.  The base of the exponentials follows
         // the maximum only when that has grown by more than 2^kSlack: weights up to 2^kSlack lose nothing (their
         // relative rounding is the same), and most tiles need no rescaling of o.
+        float mx[RT];
+        bool lead = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float mx = kNegInf;
+            mx[rt] = kNegInf;
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[rt][tt][i]);
-            mx = lane_max(mx) * a.scale_log2;
-            if (__builtin_amdgcn_ballot_w64(mx > m[rt] + kSlack || (mx > m[rt] && m[rt] == kNegInf))) {
-                const float to = fmaxf(m[rt], mx), base = to == kNegInf ? 0.f : to;
+                for (int i = 0; i < 4; ++i) mx[rt] = fmaxf(mx[rt], s[rt][tt][i]);
+            mx[rt] = lane_max(mx[rt]) * a.scale_log2;
+            lead |= mx[rt] > m[rt] + kSlack;  // (a first score is more than -inf + kSlack)
+        }
+        if (__builtin_amdgcn_ballot_w64(lead)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float to = fmaxf(m[rt], mx[rt]), base = to == kNegInf ? 0.f : to;
                 const float shrink = __builtin_amdgcn_exp2f(m[rt] - base);
                 m[rt] = to;
                 l[rt] *= shrink;
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
             }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
             const float base = m[rt] == kNegInf ? 0.f : m[rt];  // nothing attended yet: every weight is 2^-inf
             float sum = 0.f;
 #pragma unroll
@@ -403,6 +419,15 @@ __global__ __launch_bounds__(64 * row_waves(D * sizeof(T)), 2) void attn_rows_ke
                 if constexpr (kMasked) strange |= drop_nonfinite<T>(vf);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf, pf[rt], o[rt][dt]);
+            }
+        }
+        if constexpr (!kMasked) {
+            constexpr int kReads = sizeof(T) == 2 ? 2 : 4, kDeep = 4;  // the first operands are read during the softmax
+            __builtin_amdgcn_sched_group_barrier(kDsRead, kDeep * kReads, 1);
+#pragma unroll
+            for (int k = 0; k < NU * ND; ++k) {
+                __builtin_amdgcn_sched_group_barrier(kMatrix, RT * kMmaSteps, 1);
+                __builtin_amdgcn_sched_group_barrier(kDsRead, kReads, 1);
             }
         }
         // A weight of zero times an infinity or NaN is NaN: such values were left out above.  They go to the
@@ -659,7 +684,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[tt][i]);
         mx = lane_max(mx) * a.scale_log2;
-        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack || (mx > m && m == kNegInf))) {
+        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack)) {  // (a first score is more than -inf + kSlack)
             const float to = fmaxf(m, mx), base = to == kNegInf ? 0.f : to;
             const float shrink = __builtin_amdgcn_exp2f(m - base);
             m = to;
@@ -868,18 +893,24 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
     *reinterpret_cast<tw *>(static_cast<T *>(a.out) + (node * d.Hq + head) * D + lane * W) = res;
 }
 
+template <typename T, int D, int BM>
+void launch_rows(const AttnArgs &a, const AttnPlan &p, unsigned units, hipStream_t stream) {
+    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
+    hipLaunchKernelGGL((attn_rows_kernel<T, D, BM>), grid, dim3(64 * group_waves(BM)), 0, stream, a, p);
+}
+
 template <typename T, int D>
 hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-    constexpr int RB = D * sizeof(T), kWaves = row_waves(RB);
+    constexpr int RB = D * sizeof(T);
     const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
-    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units), block(64 * kWaves);
-    if (p.rows_per_group == kFewRows) {
-        if constexpr (RB < 1024)
+    if constexpr (RB < 1024)
+        if (p.rows_per_group == kFewRows)
             hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
-    } else if (p.rows_per_group == 16 * kWaves)
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, 1>), grid, block, 0, stream, a, p);
-    else if constexpr (kWaves == 4)
-        hipLaunchKernelGGL((attn_rows_kernel<T, D, 2>), grid, block, 0, stream, a, p);
+    if constexpr (RB < 512) {
+        if (p.rows_per_group == 64) launch_rows<T, D, 64>(a, p, units, stream);
+        if (p.rows_per_group == 256) launch_rows<T, D, 256>(a, p, units, stream);
+    }
+    if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
     if (p.splits > 1) {
         const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
         hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
@@ -902,7 +933,7 @@ AttnPlan attn_plan(const AttnDims &d) {
     const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
     const int64_t rows = (int64_t)d.N * d.G;
     const bool few = rows <= kFewRows && row_bytes < 1024;
-    p.rows_per_group = few ? kFewRows : row_waves(row_bytes) == 4 && rows <= 64 ? 64 : 128;
+    p.rows_per_group = few ? kFewRows : row_bytes >= 512 || (rows > 64 && rows <= 128) ? 128 : rows <= 64 ? 64 : 256;
     p.tiles = (int)((rows + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
     const int64_t least = few ? few_tile(row_bytes) * kFewWaves : 256;  // cache rows of a part
