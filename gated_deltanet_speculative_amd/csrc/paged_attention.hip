@@ -320,7 +320,8 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    constexpr int kMatrix = 0x8, kDsRead = 0x100, kMmaSteps = sizeof(T) == 2 ? 1 : 4;  // scheduling groups
+    // scheduling groups
+    constexpr int kMatrix = 0x8, kDsRead = 0x100, kArithmetic = 0x2 | 0x4 | 0x10 | 0x400, kMmaSteps = sizeof(T) == 2 ? 1 : 4;
     // One tile for this wave.  `masked`: some row does not attend to some of it.
     auto work = [&](auto masked, const char *s_k, const char *s_v, int t, unsigned long long gone) {
         constexpr bool kMasked = decltype(masked)::value;
@@ -401,34 +402,31 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
                 }
             l[rt] += sum;
         }
-        // ---- O^T += V^T P^T
+        // ---- O^T += V^T P^T, operand reads kDeep steps ahead of their products (left to itself the compiler reads
+        // one operand, waits for it and goes on); arithmetic, the exponentials of later weights among it, moves
+        // freely between the steps
         bool strange = false;
+        constexpr int kDeep = 4, kSteps = NU * ND;
+        v4i vf[kDeep], pf[RT];
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            v4i pf[RT];
+        for (int k = 0; k < kDeep; ++k) vf[k] = v_operand<T, D>(s_v, k / ND, k % ND, lane);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                if constexpr (sizeof(T) == 2)
-                    pf[rt] = Type<T>::pack(s[rt][2 * u], s[rt][2 * u + 1]);
-                else
-                    pf[rt] = __builtin_bit_cast(v4i, s[rt][u]);
+        for (int k = 0; k < kSteps; ++k) {
+            const int u = k / ND, dt = k % ND;
+            if (dt == 0) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    if constexpr (sizeof(T) == 2)
+                        pf[rt] = Type<T>::pack(s[rt][2 * u], s[rt][2 * u + 1]);
+                    else
+                        pf[rt] = __builtin_bit_cast(v4i, s[rt][u]);
+                }
             }
+            if constexpr (kMasked) strange |= drop_nonfinite<T>(vf[k % kDeep]);
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) {
-                v4i vf = v_operand<T, D>(s_v, u, dt, lane);
-                if constexpr (kMasked) strange |= drop_nonfinite<T>(vf);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf, pf[rt], o[rt][dt]);
-            }
-        }
-        if constexpr (!kMasked) {
-            constexpr int kReads = sizeof(T) == 2 ? 2 : 4, kDeep = 4;  // the first operands are read during the softmax
-            __builtin_amdgcn_sched_group_barrier(kDsRead, kDeep * kReads, 1);
-#pragma unroll
-            for (int k = 0; k < NU * ND; ++k) {
-                __builtin_amdgcn_sched_group_barrier(kMatrix, RT * kMmaSteps, 1);
-                __builtin_amdgcn_sched_group_barrier(kDsRead, kReads, 1);
-            }
+            for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf[k % kDeep], pf[rt], o[rt][dt]);
+            if (k + kDeep < kSteps) vf[k % kDeep] = v_operand<T, D>(s_v, (k + kDeep) / ND, (k + kDeep) % ND, lane);
+            if constexpr (!kMasked) __builtin_amdgcn_sched_barrier(kArithmetic);
         }
         // A weight of zero times an infinity or NaN is NaN: such values were left out above.  They go to the
         // rows that do attend to them by two products of ones (values of +inf or NaN, of -inf or NaN) with
