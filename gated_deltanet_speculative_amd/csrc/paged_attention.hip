@@ -311,6 +311,14 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
         }
     };
 
+    // The rows of the tile behind t, and the page ids of the one behind that
+    auto request = [&](int t) {
+        if (t + TOK < t1) {
+            load(t + TOK);
+            lookup(t + 2 * TOK);
+        }
+    };
+
     v4f o[RT][ND];
     float m[RT], l[RT];
 #pragma unroll
@@ -320,11 +328,11 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    // scheduling groups
-    constexpr int kMatrix = 0x8, kDsRead = 0x100, kArithmetic = 0x2 | 0x4 | 0x10 | 0x400, kMmaSteps = sizeof(T) == 2 ? 1 : 4;
+    constexpr int kMatrix = 0x8, kDsRead = 0x100, kMmaSteps = sizeof(T) == 2 ? 1 : 4;  // scheduling groups
     // One tile for this wave.  `masked`: some row does not attend to some of it.
     auto work = [&](auto masked, const char *s_k, const char *s_v, int t, unsigned long long gone) {
         constexpr bool kMasked = decltype(masked)::value;
+        request(t);
         // ---- S^T = K Q^T
         v4f s[RT][NT];
 #pragma unroll
@@ -389,25 +397,25 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
                 for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
             }
         }
+        float base[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float base = m[rt] == kNegInf ? 0.f : m[rt];  // nothing attended yet: every weight is 2^-inf
-            float sum = 0.f;
-#pragma unroll
-            for (int tt = 0; tt < NT; ++tt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[rt][tt][i] = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], a.scale_log2, -base));
-                    sum += s[rt][tt][i];
-                }
-            l[rt] += sum;
-        }
+        for (int rt = 0; rt < RT; ++rt) base[rt] = m[rt] == kNegInf ? 0.f : m[rt];  // nothing attended yet: every weight is 2^-inf
+        auto weigh = [&](int rt, int e) {  // score e of this lane becomes its weight
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][e >> 2][e & 3], a.scale_log2, -base[rt]));
+            s[rt][e >> 2][e & 3] = x;
+            l[rt] += x;
+        };
         // ---- O^T += V^T P^T, operand reads kDeep steps ahead of their products (left to itself the compiler reads
-        // one operand, waits for it and goes on); arithmetic, the exponentials of later weights among it, moves
-        // freely between the steps
+        // one operand, waits for it and goes on), and the weights of the next step of the contraction a few at a
+        // time beside the products of this one
         bool strange = false;
         constexpr int kDeep = 4, kSteps = NU * ND;
+        constexpr int kScores = 4 * NT / NU, kPart = (kScores + ND - 1) / ND;  // a step's scores per query row, and per product
         v4i vf[kDeep], pf[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < kScores; ++e) weigh(rt, e);
 #pragma unroll
         for (int k = 0; k < kDeep; ++k) vf[k] = v_operand<T, D>(s_v, k / ND, k % ND, lane);
 #pragma unroll
@@ -426,7 +434,12 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf[k % kDeep], pf[rt], o[rt][dt]);
             if (k + kDeep < kSteps) vf[k % kDeep] = v_operand<T, D>(s_v, (k + kDeep) / ND, (k + kDeep) % ND, lane);
-            if constexpr (!kMasked) __builtin_amdgcn_sched_barrier(kArithmetic);
+            if (u + 1 < NU)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = kPart * dt; e < kPart * dt + kPart && e < kScores; ++e) weigh(rt, kScores * (u + 1) + e);
+            if constexpr (!kMasked) __builtin_amdgcn_sched_barrier(0);
         }
         // A weight of zero times an infinity or NaN is NaN: such values were left out above.  They go to the
         // rows that do attend to them by two products of ones (values of +inf or NaN, of -inf or NaN) with
@@ -472,7 +485,7 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
     load(t0);
     lookup(t0 + TOK);
     lds_barrier();
-    // Writes the loaded tile to LDS, requests the next one and waits for the workgroup: the tile's absent rows.
+    // Writes the loaded tile to LDS and waits for the workgroup: the tile's absent rows.
     int n3 = 0;
     auto turn = [&](int t, char *s_k, char *s_v) {
         if (unpaged) {
@@ -497,10 +510,6 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
         const int here = n3;
         n3 = n3 == 2 ? 0 : n3 + 1;
         if (tid == 0) s_absent[n3] = 0;
-        if (t + TOK < t1) {
-            load(t + TOK);
-            lookup(t + 2 * TOK);
-        }
         lds_barrier();
         return s_absent[here];
     };
@@ -516,12 +525,18 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
             turned = true;
             break;
         }
-        if (working) work(std::false_type{}, s_kv[half][0], s_kv[half][1], t, 0ull);
+        if (working)
+            work(std::false_type{}, s_kv[half][0], s_kv[half][1], t, 0ull);
+        else
+            request(t);
     }
     for (; t < t1; t += TOK, half ^= 1) {
         if (!turned) gone = turn(t, s_kv[half][0], s_kv[half][1]);
         turned = false;
-        if (working && (tree || t <= L + last_token)) work(std::true_type{}, s_kv[half][0], s_kv[half][1], t, gone);
+        if (working && (tree || t <= L + last_token))
+            work(std::true_type{}, s_kv[half][0], s_kv[half][1], t, gone);
+        else
+            request(t);
     }
 
     // ---- results: lane holds columns 16 dt + 4g .. + 3 of its query row
