@@ -22,6 +22,9 @@ namespace gdn {
 namespace {
 
 constexpr float kNegInf = -__builtin_inff();
+// What may be scheduled across a step of the products: vector, scalar and transcendental arithmetic and global
+// memory, not the LDS reads and products themselves, whose order is the reading ahead.
+constexpr int kArithmetic = 0x2 | 0x4 | 0x10 | 0x400;
 constexpr float kSlack = 6.f;  // how far, in powers of two, a running maximum may lead its base
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
@@ -188,6 +191,26 @@ __device__ inline v4f load4(const T *p) {
 }
 __device__ inline float gated(float o, float z, int mode) { return o * (mode == 0 ? fast_silu(z) : fast_sigmoid(z)); }
 
+// The cache rows of a tile of at most 64: lane j of a wave finds row t + j from its page id (requested a tile
+// earlier), the others' rows come by a lane shuffle.  `have`: the rows before t1 that lie in a page of the pool, as a
+// bit set, the same in every wave; any other row stands for the pool's first one, so that every load is in bounds.
+struct TileRows {
+    unsigned long long have;
+    uint32_t mine;
+    __device__ uint32_t at(int j) const { return (uint32_t)__shfl((int)mine, j); }
+};
+template <int kTok>
+__device__ inline TileRows tile_rows_of(const AttnDims &d, int t, int t1, int pid, int h) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t tk = t + lane;
+    const bool ok = (lane < kTok) & ((int)tk < t1) & ((unsigned)pid < (unsigned)d.n_pages);
+    return TileRows{__builtin_amdgcn_ballot_w64(ok), ok ? cache_row(d, pid, h, tk, d.page(tk)) : 0u};
+}
+template <int kTok>
+__device__ inline unsigned long long rows_absent(unsigned long long have, int t, int t1) {
+    return low_bits(min(kTok, t1 - t)) & ~have;
+}
+
 // What a workgroup leaves for the join, one pair per (split, query row) behind the partial outputs: the running
 // maximum and sum; maximum -inf and sum 0 where the part holds nothing; a NaN maximum where the row is absent or its
 // lane is not computed, so that the join looks at nothing else of the lane.
@@ -216,9 +239,6 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
     static_assert(BM == 16 * RT * kWaves && RPP <= TOK, "");
     constexpr int NU = sizeof(T) == 2 ? TOK / 32 : TOK / 16;
     __shared__ __attribute__((aligned(16))) char s_kv[2][2][TOK * RB];
-    // cache rows of a tile that lie in no page of the pool: by tile number mod 3 (written before the
-    // tile's barrier, read behind it, cleared before the barrier of the second tile after it)
-    __shared__ unsigned long long s_absent[3];
 
     const AttnDims &d = a.d;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4;
@@ -286,36 +306,26 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
     // ---- staging: thread tid carries chunk tid % TPR of rows tid / TPR + RPP p of the tile
     const int32_t *table = a.l.page_table + (int64_t)ln.slot * d.max_pages;
     const int chunk = tid % TPR, row_in = tid / TPR;
-    int pid[NP];
     v4i kr[NP], vr[NP];
-    auto lookup = [&](int t) {
+    auto lookup = [&](int t) { return table[d.page((uint32_t)min(t + lane, t1 - 1))]; };
+    auto load = [&](int t, int pid) {
+        const TileRows rows = tile_rows_of<TOK>(d, t, t1, pid, h);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int tk = t + row_in + RPP * p;
-            pid[p] = table[d.page((uint32_t)min(tk, t1 - 1))];  // (not looked at before the load: nothing waits for it here)
-        }
-    };
-    // (a row without a page is loaded from the pool's first row and cleared before it is used)
-    unsigned unpaged = 0;
-    auto load = [&](int t) {
-        unpaged = 0;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const uint32_t tk = t + row_in + RPP * p;
-            const bool ok = (int)tk < t1 & (unsigned)pid[p] < (unsigned)d.n_pages;
-            const uint32_t row = ok ? cache_row(d, pid[p], h, tk, d.page(tk)) : 0u;
-            unpaged |= ok ? 0u : 1u << p;
-            const size_t at = (size_t)row * RB + chunk * 16;
+            const size_t at = (size_t)rows.at(row_in + RPP * p) * RB + chunk * 16;
             kr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at);
             vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
         }
+        return rows.have;
     };
-
     // The rows of the tile behind t, and the page ids of the one behind that
+    int pid = lookup(t0);
+    unsigned long long have = load(t0, pid);
+    pid = lookup(t0 + TOK);
     auto request = [&](int t) {
         if (t + TOK < t1) {
-            load(t + TOK);
-            lookup(t + 2 * TOK);
+            have = load(t + TOK, pid);
+            pid = lookup(t + 2 * TOK);
         }
     };
 
@@ -328,27 +338,29 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    constexpr int kMatrix = 0x8, kDsRead = 0x100, kMmaSteps = sizeof(T) == 2 ? 1 : 4;  // scheduling groups
     // One tile for this wave.  `masked`: some row does not attend to some of it.
     auto work = [&](auto masked, const char *s_k, const char *s_v, int t, unsigned long long gone) {
         constexpr bool kMasked = decltype(masked)::value;
         request(t);
         // ---- S^T = K Q^T
         v4f s[RT][NT];
+        constexpr int kDeep = 4;  // operands read ahead of their products
+        {
+            constexpr int kSteps = NS * NT;  // (contraction outermost: the products of one score tile depend on each other)
+            auto operand = [&](int k) {
+                return *reinterpret_cast<const v4i *>(s_k + lds_at<RB>(16 * (k % NT) + (lane & 15), 4 * (k / NT) + g));
+            };
+            v4i kf[kDeep];
 #pragma unroll
-        for (int ks = 0; ks < NS; ++ks)  // (outermost: the products of one tile depend on each other)
+            for (int k = 0; k < kDeep; ++k) kf[k] = operand(k);
 #pragma unroll
-            for (int tt = 0; tt < NT; ++tt) {
-                const v4i kf = *reinterpret_cast<const v4i *>(s_k + lds_at<RB>(16 * tt + (lane & 15), 4 * ks + g));
+            for (int k = 0; k < kSteps; ++k) {
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) s[rt][tt] = Type<T>::mma(kf, qf[rt][ks], ks ? s[rt][tt] : v4f{0.f, 0.f, 0.f, 0.f});
+                for (int rt = 0; rt < RT; ++rt)
+                    s[rt][k % NT] = Type<T>::mma(kf[k % kDeep], qf[rt][k / NT], k >= NT ? s[rt][k % NT] : v4f{0.f, 0.f, 0.f, 0.f});
+                if (k + kDeep < kSteps) kf[k % kDeep] = operand(k + kDeep);
+                __builtin_amdgcn_sched_barrier(kArithmetic);
             }
-        // operand reads two steps ahead of their products
-        __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * NT, 0);
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-            __builtin_amdgcn_sched_group_barrier(kMatrix, NT * RT * kMmaSteps, 0);
-            __builtin_amdgcn_sched_group_barrier(kDsRead, NT, 0);
         }
         // ---- rows that are not attended weigh nothing, whatever their scores are: the tile's rows that a query
         // row attends to as a bit set, shifted so that this lane's rows are bits 16 tt + i
@@ -409,7 +421,7 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
         // one operand, waits for it and goes on), and the weights of the next step of the contraction a few at a
         // time beside the products of this one
         bool strange = false;
-        constexpr int kDeep = 4, kSteps = NU * ND;
+        constexpr int kSteps = NU * ND;
         constexpr int kScores = 4 * NT / NU, kPart = (kScores + ND - 1) / ND;  // a step's scores per query row, and per product
         v4i vf[kDeep], pf[RT];
 #pragma unroll
@@ -480,26 +492,17 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
             }
     };
 
-    if (tid < 3) s_absent[tid] = 0;
-    lookup(t0);
-    load(t0);
-    lookup(t0 + TOK);
-    lds_barrier();
-    // Writes the loaded tile to LDS and waits for the workgroup: the tile's absent rows.
-    int n3 = 0;
+    // Writes the loaded tile to LDS (rows without a page as zeros) and waits for the workgroup: the tile's absent rows.
     auto turn = [&](int t, char *s_k, char *s_v) {
-        if (unpaged) {
-            unsigned long long absent = 0;  // rows of this part without a page: not attended, reported
+        const unsigned long long gone = rows_absent<TOK>(have, t, t1);
+        if (gone || t + TOK > t1) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-                if ((unpaged >> p) & 1) {
-                    kr[p] = vr[p] = v4i{0, 0, 0, 0};
-                    absent |= t + row_in + RPP * p < t1 ? 1ull << (row_in + RPP * p) : 0ull;
-                }
-            if (absent) {
-                atomicOr(&s_absent[n3], absent);
-                if (a.l.status) atomicOr(a.l.status, GDN_STATUS_PAGE);
+            for (int p = 0; p < NP; ++p) {
+                const bool ok = (have >> (row_in + RPP * p)) & 1;
+                kr[p] = v4i{ok ? kr[p][0] : 0, ok ? kr[p][1] : 0, ok ? kr[p][2] : 0, ok ? kr[p][3] : 0};
+                vr[p] = v4i{ok ? vr[p][0] : 0, ok ? vr[p][1] : 0, ok ? vr[p][2] : 0, ok ? vr[p][3] : 0};
             }
+            if (gone && tid == 0 && a.l.status) atomicOr(a.l.status, GDN_STATUS_PAGE);
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -507,11 +510,8 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
             *reinterpret_cast<v4i *>(s_k + at) = kr[p];
             *reinterpret_cast<v4i *>(s_v + at) = vr[p];
         }
-        const int here = n3;
-        n3 = n3 == 2 ? 0 : n3 + 1;
-        if (tid == 0) s_absent[n3] = 0;
         lds_barrier();
-        return s_absent[here];
+        return gone;
     };
     // First the tiles that every row of the workgroup attends to throughout, without a trace of the masks; from
     // the first other one on (the diagonal, the draft tree, a row without a page) the tiles with masks.
@@ -563,6 +563,324 @@ __global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(Attn
         const int head = h * d.G + r - token[rt] * d.G;
         T *out = static_cast<T *>(a.out) + (node * d.Hq + head) * D;
         const T *z = static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) {
+            v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o[rt][dt] * inv;
+            if (a.gate.p) {
+                const v4f zz = load4(z + 16 * dt + 4 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = gated(v[i], zz[i], a.gate_mode);
+            }
+            store4(out + 16 * dt + 4 * g, v);
+        }
+    }
+}
+
+// Wide rows (512 bytes: 16-bit values of 256 columns), more query rows than the kernel for few.
+//
+// A wave that owns 32 query rows of this width would hold 128 registers of outputs and 64 of queries, and one that
+// owns 16 reads 64 bytes of LDS per product instruction, twice what the LDS delivers.  So a pair of waves shares 32
+// query rows: each computes the scores of one half of a tile's 64 cache rows against the whole width, the pair
+// exchanges its rows' maxima and the weights (8 KiB a tile through LDS), and each multiplies all of the weights with
+// its half of the columns of V.  Per product a wave reads half as much LDS as with 16 rows, and holds 64 registers
+// of outputs.  Two barriers a tile: behind the maxima, where K has been read and V of the tile is written, and behind
+// the weights, where K of the next tile is.
+constexpr int kPairRows = 128, kPairThreads = 512;
+
+template <typename T>
+__global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, AttnPlan plan) {
+    constexpr int D = 256, RB = 512, TOK = 64, RT = 2, NT = 2, NS = RB / 64, ND = 8;  // NT, ND: of this wave's half
+    constexpr int BM = kPairRows, TPR = RB / 16, RPP = kPairThreads / TPR, NP = TOK / RPP;
+    static_assert(sizeof(T) == 2, "");
+    __shared__ __attribute__((aligned(16))) char s_k[TOK * RB], s_vs[2][TOK * RB];
+    __shared__ v4i s_p[4][2][RT][64];              // weights as operands: [pair][half][row tile][lane]
+    __shared__ float s_mx[4][2][16 * RT], s_l[4][2][16 * RT];
+
+    const AttnDims &d = a.d;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, n = lane & 15, pair = wave >> 1, hf = wave & 1;
+    const bool tree = a.l.parents != nullptr;
+    unsigned b = blockIdx.x;  // (units of work as in the row kernel)
+    const unsigned units = (unsigned)d.C * d.Hkv * plan.tiles * plan.splits;
+    if (plan.tiles > 1) b = (b & 7) * (gridDim.x >> 3) + (b >> 3);
+    if (b >= units) return;
+    const int split = b % plan.splits, tile = plan.tiles - 1 - (b / plan.splits) % plan.tiles;
+    const int ch = b / (plan.splits * plan.tiles), h = ch % d.Hkv, c = ch / d.Hkv, r0 = tile * BM;
+    const float skip = __builtin_nanf("");
+    const Lane ln = paged_lane(d, a.l, c);
+    if (ln.slot == -1) {
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, r0, BM, skip);
+        return;
+    }
+    int bits = ln.bits;
+    unsigned anc = 0;
+    if (tree && !(bits & GDN_STATUS_NODES)) {
+        bool bad;
+        anc = tree_ancestors(a.l.parents + (int64_t)c * d.N, ln.nodes, bad);
+        if (bad) bits |= GDN_STATUS_PARENT;
+    }
+    if (bits) {
+        if (a.l.status && split == 0 && tile == 0 && h == 0 && tid == 0) atomicOr(a.l.status, bits);
+        if (plan.splits > 1) leave_nothing(a, plan, split, c, h, r0, BM, skip);
+        return;
+    }
+    const int rows = ln.nodes * d.G, L = ln.len;
+    if (plan.splits > 1 && rows < r0 + BM) leave_nothing(a, plan, split, c, h, max(r0, rows), BM, skip);
+    if (r0 >= rows) return;
+    const Reach rc = reach(tree, L, ln.nodes, (r0 + BM - 1) / d.G, plan.splits, TOK);
+    const int t0 = split * rc.part, t1 = min(t0 + rc.part, rc.end);
+    if (t0 >= t1) {  // (only with several splits)
+        leave_nothing(a, plan, split, c, h, r0, min(BM, rows - r0), kNegInf);
+        return;
+    }
+
+    // ---- the pair's query rows and what they attend to
+    const int rw = r0 + pair * 16 * RT;
+    const bool working = rw < rows;
+    const int last_token = min(rw + 16 * RT - 1, rows - 1) / d.G;
+    v4i qf[RT][NS];
+    int token[RT];
+    unsigned sees[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rw + 16 * rt + n;
+        token[rt] = min(r, rows - 1) / d.G;
+        sees[rt] = __shfl(anc, token[rt] & 63);
+        const int gh = min(r, rows - 1) - token[rt] * d.G;
+        const T *q = static_cast<const T *>(a.q) + (((int64_t)c * d.N + token[rt]) * d.Hq + h * d.G + gh) * D;
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) {
+            const v4i v = *reinterpret_cast<const v4i *>(reinterpret_cast<const char *>(q) + 64 * ks + 16 * g);
+            qf[rt][ks] = r < rows ? v : v4i{0, 0, 0, 0};
+        }
+    }
+
+    // ---- staging as in the row kernel, K and V in turns, so that 16 registers are in use for it at any time
+    const int32_t *table = a.l.page_table + (int64_t)ln.slot * d.max_pages;
+    const int chunk = tid % TPR, row_in = tid / TPR;
+    v4i kr[NP], vr[NP];
+    auto lookup = [&](int t) { return table[d.page((uint32_t)min(t + lane, t1 - 1))]; };
+    auto load = [&](const TileRows &rows, const void *cache, v4i *to) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            to[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(cache) + (size_t)rows.at(row_in + RPP * p) * RB + chunk * 16);
+    };
+    auto stage = [&](v4i *from, unsigned long long have, char *to) {  // (rows without a page as zeros)
+        if (have != ~0ull)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const bool ok = (have >> (row_in + RPP * p)) & 1;
+                from[p] = v4i{ok ? from[p][0] : 0, ok ? from[p][1] : 0, ok ? from[p][2] : 0, ok ? from[p][3] : 0};
+            }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<v4i *>(to + lds_at<RB>(row_in + RPP * p, chunk)) = from[p];
+    };
+
+    v4f o[RT][ND];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kNegInf;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) o[rt][dt] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    constexpr int kDeep = 4;  // operands read ahead of their products
+
+    // One tile.  `active`: this pair attends to some of it.  Every wave of the workgroup passes both barriers.
+    TileRows now{}, next{};  // of the tile at hand, and of the one behind it
+    int pid = lookup(t0);
+    auto step = [&](auto masked, int t, char *s_v, bool active) {
+        constexpr bool kMasked = decltype(masked)::value;
+        const bool more = t + TOK < t1;
+        if (more) {
+            next = tile_rows_of<TOK>(d, t + TOK, t1, pid, h);
+            load(next, a.k_cache, kr);
+        }
+        v4f s[RT][NT];
+        unsigned long long see[RT];
+        float mx[RT];
+        if (active) {
+            constexpr int kSteps = NS * NT;
+            auto operand = [&](int k) {
+                return *reinterpret_cast<const v4i *>(s_k + 32 * hf * RB + lds_at<RB>(16 * (k % NT) + n, 4 * (k / NT) + g));
+            };
+            v4i kf[kDeep];
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) kf[k] = operand(k);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    s[rt][k % NT] = Type<T>::mma(kf[k % kDeep], qf[rt][k / NT], k >= NT ? s[rt][k % NT] : v4f{0.f, 0.f, 0.f, 0.f});
+                if (k + kDeep < kSteps) kf[k % kDeep] = operand(k + kDeep);
+                __builtin_amdgcn_sched_barrier(kArithmetic);
+            }
+            if constexpr (kMasked) {
+                int g4 = 4 * g;
+                asm volatile("" : "+v"(g4));  // (keeps what follows out of the other tiles' registers)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int rel = L - t;
+                    unsigned long long x = low_bits(min(tree ? rel : rel + token[rt] + 1, t1 - t));
+                    if (tree) {
+                        const unsigned long long nodes = sees[rt];
+                        x |= (rel >= 64 || rel <= -32 ? 0 : rel >= 0 ? nodes << rel : nodes >> -rel) & low_bits(t1 - t);
+                    }
+                    see[rt] = (x & now.have) >> g4;
+                    const unsigned mine = (unsigned)(see[rt] >> (32 * hf));
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[rt][tt][i] = (mine >> (16 * tt + i)) & 1 ? s[rt][tt][i] : kNegInf;
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                mx[rt] = kNegInf;
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[rt] = fmaxf(mx[rt], s[rt][tt][i]);
+                mx[rt] = lane_max(mx[rt]) * a.scale_log2;
+                if (g == 0) s_mx[pair][hf][16 * rt + n] = mx[rt];
+            }
+        }
+        stage(vr, now.have, s_v);
+        lds_barrier();  // K has been read; the maxima and this tile's V are there
+        v4i pf[RT];
+        if (active) {
+            bool lead = false;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {  // both waves of the pair come to the same maxima and bases
+                mx[rt] = fmaxf(mx[rt], s_mx[pair][hf ^ 1][16 * rt + n]);
+                lead |= mx[rt] > m[rt] + kSlack;
+            }
+            if (__builtin_amdgcn_ballot_w64(lead)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float to = fmaxf(m[rt], mx[rt]), base = to == kNegInf ? 0.f : to;
+                    const float shrink = __builtin_amdgcn_exp2f(m[rt] - base);
+                    m[rt] = to;
+                    l[rt] *= shrink;
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float base = m[rt] == kNegInf ? 0.f : m[rt];
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], a.scale_log2, -base));
+                        s[rt][tt][i] = x;
+                        l[rt] += x;
+                    }
+                pf[rt] = Type<T>::pack(s[rt][0], s[rt][1]);
+                s_p[pair][hf][rt][lane] = pf[rt];
+            }
+        }
+        if (more) {
+            stage(kr, next.have, s_k);
+            load(next, a.v_cache, vr);
+            pid = lookup(t + 2 * TOK);
+            if (tid == 0 && a.l.status && rows_absent<TOK>(next.have, t + TOK, t1)) atomicOr(a.l.status, GDN_STATUS_PAGE);
+        }
+        now = next;
+        lds_barrier();  // the weights and the next tile's K are there
+        if (!active) return;
+        // ---- O^T += V^T P^T: this wave's half of the columns, its own weights first, then the partner's
+        bool strange = false;
+        constexpr int kSteps = 2 * ND;
+        v4i vf[kDeep], other[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) other[rt] = s_p[pair][hf ^ 1][rt][lane];
+        auto operand = [&](int k) { return v_operand<T, D>(s_v + 32 * RB * (k < ND ? hf : hf ^ 1), 0, 8 * hf + k % ND, lane); };
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) vf[k] = operand(k);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if constexpr (kMasked) strange |= drop_nonfinite<T>(vf[k % kDeep]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[rt][k % ND] = Type<T>::mma(vf[k % kDeep], k < ND ? pf[rt] : other[rt], o[rt][k % ND]);
+            if (k + kDeep < kSteps) vf[k % kDeep] = operand(k + kDeep);
+            if constexpr (!kMasked) __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kMasked)  // infinities and NaN go to the rows that attend to them, as in the row kernel
+            if (__builtin_amdgcn_ballot_w64(strange)) {
+#pragma unroll 1
+                for (int side = 0; side < 4; ++side) {  // +inf and -inf, in either half of the tile
+                    const float inf = side & 1 ? kNegInf : -kNegInf;
+                    const int half = side >> 1;
+                    v4i reads[RT];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const unsigned at = (unsigned)(see[rt] >> (32 * half));
+                        v4f one[2];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) one[j >> 2][j & 3] = (at >> (16 * (j >> 2) + (j & 3))) & 1 ? 1.f : 0.f;
+                        reads[rt] = Type<T>::pack(one[0], one[1]);
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) {
+                        const v4i f = nonfinite_ones<T>(v_operand<T, D>(s_v + 32 * RB * half, 0, 8 * hf + dt, lane), side & 1);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const v4f cnt = Type<T>::mma(f, reads[rt], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[rt][dt][i] += cnt[i] > 0.f ? inf : 0.f;
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+    };
+
+    now = tile_rows_of<TOK>(d, t0, t1, pid, h);
+    load(now, a.k_cache, kr);
+    load(now, a.v_cache, vr);
+    pid = lookup(t0 + TOK);
+    if (tid == 0 && a.l.status && rows_absent<TOK>(now.have, t0, t1)) atomicOr(a.l.status, GDN_STATUS_PAGE);
+    stage(kr, now.have, s_k);
+    lds_barrier();
+    // full tiles first, then, from the first one with a mask or an absent row on, the tiles with masks
+    const int all_see = min(tree ? L : L + r0 / d.G + 1, t1);
+    int t = t0, half = 0;
+    for (; t + TOK <= all_see && now.have == ~0ull; t += TOK, half ^= 1) step(std::false_type{}, t, s_vs[half], working);
+    for (; t < t1; t += TOK, half ^= 1) step(std::true_type{}, t, s_vs[half], working && (tree || t <= L + last_token));
+
+    // ---- results: this wave's half of the columns
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        l[rt] = lane_sum(l[rt]);
+        if (g == 0) s_l[pair][hf][16 * rt + n] = l[rt];
+    }
+    lds_barrier();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rw + 16 * rt + n;
+        // (the halves' sums in one order for both waves)
+        const float sum = s_l[pair][0][16 * rt + n] + s_l[pair][1][16 * rt + n];
+        if (r >= rows) continue;
+        if (plan.splits > 1) {
+            const size_t row = (size_t)split * all_rows + ((size_t)c * d.Hkv + h) * d.N * d.G + r;
+            float *po = a.workspace + row * D + 128 * hf;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) *reinterpret_cast<v4f *>(po + 16 * dt + 4 * g) = o[rt][dt];
+            if (g == 0 && hf == 0) {
+                float *ml = join_pairs(a, plan) + row * 2;
+                ml[0] = m[rt];
+                ml[1] = sum;
+            }
+            continue;
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const int64_t node = (int64_t)c * d.N + token[rt];
+        const int head = h * d.G + r - token[rt] * d.G;
+        T *out = static_cast<T *>(a.out) + (node * d.Hq + head) * D + 128 * hf;
+        const T *z = static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head + 128 * hf;
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
             v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o[rt][dt] * inv;
@@ -643,27 +961,24 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
         for (int ks = 0; ks < NS; ++ks) qf[ks] = *reinterpret_cast<const v4i *>(q + 64 * ks + 16 * g);
     }
 
-    // ---- cache rows of a tile: lane j finds row t + j
     const int32_t *table = a.l.page_table + (int64_t)ln.slot * d.max_pages;
     auto fetch = [&](int t) { return table[d.page((uint32_t)min(t + lane, t1 - 1))]; };
     v4i kr[NT * NS], vr[NP];
-    auto load = [&](int t, int pid) {  // the tile's rows with a page, as a bit set; the others are loaded from row 0
-        const uint32_t tk = t + lane;
-        const bool ok = lane < TOK && (int)tk < t1 && (unsigned)pid < (unsigned)d.n_pages;
-        const uint32_t mine = ok ? cache_row(d, pid, h, tk, d.page(tk)) : 0u;
+    auto load = [&](int t, int pid) {
+        const TileRows rows = tile_rows_of<TOK>(d, t, t1, pid, h);
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt) {
-            const size_t at = (size_t)(uint32_t)__shfl((int)mine, 16 * tt + n) * RB + 16 * g;
+            const size_t at = (size_t)rows.at(16 * tt + n) * RB + 16 * g;
 #pragma unroll
             for (int ks = 0; ks < NS; ++ks)
                 kr[tt * NS + ks] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.k_cache) + at + 64 * ks);
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const size_t at = (size_t)(uint32_t)__shfl((int)mine, RPP * p + lane / TPR) * RB + 16 * (lane % TPR);
+            const size_t at = (size_t)rows.at(RPP * p + lane / TPR) * RB + 16 * (lane % TPR);
             vr[p] = *reinterpret_cast<const v4i *>(static_cast<const char *>(a.v_cache) + at);
         }
-        return __builtin_amdgcn_ballot_w64(ok);
+        return rows.have;
     };
 
     v4f o[ND];
@@ -923,7 +1238,13 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
         if (p.rows_per_group == 64) launch_rows<T, D, 64>(a, p, units, stream);
         if (p.rows_per_group == 256) launch_rows<T, D, 256>(a, p, units, stream);
     }
-    if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
+    if constexpr (D == 256 && sizeof(T) == 2) {
+        if (p.rows_per_group == kPairRows)
+            hipLaunchKernelGGL((attn_pair_kernel<T>), dim3(p.tiles > 1 ? (units + 7) / 8 * 8 : units), dim3(kPairThreads), 0,
+                               stream, a, p);
+    } else {
+        if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
+    }
     if (p.splits > 1) {
         const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
         hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
