@@ -247,3 +247,84 @@ def test_graph_replay_follows_lengths_and_inputs():
         torch.cuda.synchronize()
         assert torch.equal(out, want), f"replay {k}"
     assert int(status.item()) == 0
+
+
+# Head layouts that reach every kernel: few rows, 64, 128 and 256 rows a workgroup, pairs of waves, each type
+KERNELS = [(64, 2), (64, 8), (64, 16), (64, 40), (128, 2), (128, 8), (128, 16), (128, 40), (256, 1), (256, 2), (256, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+@pytest.mark.parametrize("tree", [False, True])
+def test_poisoned_rows_in_every_kernel(dtype, D, G, tree):
+    """As above, with a cache of several tiles, lanes of different lengths and a part that ends inside a tile: the
+    nodes that attend to a poisoned row are not finite, the others are what they are without it."""
+    C, N, page, lens = 2, 8, 48, [150, 61]
+    pg = Paged(C, N, G, 1, D, page, dtype, lens, seed=D + G)
+    q = pg.normal(C, N, G, D)
+    parents = np.array([[-1, 0, 0, 1, 1, 2, -1, 6]] * C, np.int32) if tree else None
+    clean, res, status, bits = _run(pg, q, parents)
+    assert status == bits == 0
+    check_attention(clean, res, dtype)
+    poisoned = 2
+    for c in range(C):
+        s, n = int(pg.slots[c]), lens[c]
+        for t in (n + poisoned, *range(n + N, pg.table.shape[1] * page)):
+            pid = int(pg.table[s, t // page])
+            if pid >= 0:
+                pg.k[pid, :, t % page] = float("nan")
+                pg.v[pid, :, t % page] = float("-inf") if c else float("nan")
+    out = torch.full((C, N, G, D), SENTINEL, dtype=dtype, device="cuda")
+    gdn.paged_attention(pg.sh, q, pg.k, pg.v, *pg.places(), parents=None if parents is None else dev(parents), out=out)
+    seen = [i for i in range(N) if poisoned in R.path_of(None if parents is None else parents[0], i)]
+    keep = [i for i in range(N) if i not in seen]
+    got = as_numpy(out)
+    assert not np.isfinite(got[:, seen]).any()
+    assert np.array_equal(got[:, keep], as_numpy(clean)[:, keep])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+def test_infinite_values_in_every_kernel(dtype, D, G):
+    """Infinite values (finite keys) of the chain's own rows reach exactly the nodes that attend to them, in their
+    column and with their sign, and NaN where both signs meet."""
+    N, L = 6, 100
+    pg = Paged(1, N, G, 1, D, 32, dtype, [L], seed=3 * D + G)
+    q = pg.normal(1, N, G, D)
+    clean = as_numpy(_run(pg, q)[0])
+
+    def put(node, col, value):
+        pg.v[int(pg.table[pg.slots[0], (L + node) // 32]), 0, (L + node) % 32, col] = value
+
+    put(1, 3, float("inf"))
+    put(3, D - 1, float("-inf"))
+    put(2, 17, float("inf"))
+    put(4, 17, float("-inf"))
+    got = as_numpy(_run(pg, q)[0]).copy()
+    assert np.isposinf(got[0, 1:, :, 3]).all() and np.isneginf(got[0, 3:, :, D - 1]).all()
+    assert np.isposinf(got[0, 2:4, :, 17]).all() and np.isnan(got[0, 4:, :, 17]).all()
+    for i, col in ((1, 3), (3, D - 1), (2, 17)):
+        got[0, i:, :, col] = clean[0, i:, :, col]
+    assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunks_behind_long_caches(dtype, D):
+    """Row tiles of every width over caches of many tiles, ragged and padded, with a gate."""
+    _case(3, 70, 6, 2, D, 48, dtype, [700, 0, 321], ragged=True, gate=1, seed=D)
+    _case(1, 33, 8, 1, D, 64, dtype, [1500], seed=D + 1)
+    _case(2, 3, 12, 2, D, 16, dtype, [2000, 1], seed=D + 2)
+
+
+@pytest.mark.parametrize("D,G,N", [(64, 4, 3), (64, 8, 8), (128, 16, 8), (128, 40, 8), (256, 2, 8), (256, 40, 8)])
+def test_absent_pages_in_every_kernel(D, G, N):
+    """Pages outside the pool in the first, a middle and the last place: their rows count as not attended to."""
+    pg = Paged(2, N, G, 1, D, 16, BF, [200, 700], seed=D + G + 1)
+    q = pg.normal(2, N, G, D)
+    for at in (0, 5, (200 + N - 1) // 16):
+        table = pg.table.copy()
+        table[pg.slots[0], at] = pg.sh.n_pages + 3
+        out, res, status, bits = _run(pg, q, table=table)
+        assert status == R.PAGE and bits == R.PAGE
+        check_attention(out, res, BF, ctx=f"page {at}")
