@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -21,7 +22,7 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ROUND_EXPORTED = ("gdn_rope_kv_write", "gdn_paged_attention", "gdn_paged_attention_workspace_size",
                   "gdn_draft_accept", "gdn_draft_accept_workspace_size", "gdn_kv_commit_layers")
 
-_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_i32, _vp = ctypes.c_int32, ctypes.c_void_p
 
 
 class _CAttnShape(ctypes.Structure):
@@ -31,10 +32,6 @@ class _CAttnShape(ctypes.Structure):
 
 class _CAcceptShape(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("n_seqs", "n_nodes", "vocab", "dtype")]
-
-
-class _CView(ctypes.Structure):
-    _fields_ = [("p", _vp), ("token_stride", _i64), ("head_stride", _i64)]
 
 
 class _CRope(ctypes.Structure):
@@ -91,9 +88,9 @@ def _library():
     global _calls
     if _calls is None:
         lib = load_library()
-        sp, ap, vp = ctypes.POINTER(_CAttnShape), ctypes.POINTER(_CAcceptShape), ctypes.POINTER(_CView)
-        lib.gdn_rope_kv_write.argtypes = [sp, _i32, vp, vp, vp, ctypes.POINTER(_CRope)] + [_vp] * 10
-        lib.gdn_paged_attention.argtypes = [sp] + [_vp] * 8 + [ctypes.c_float, vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        sp, ap = ctypes.POINTER(_CAttnShape), ctypes.POINTER(_CAcceptShape)
+        lib.gdn_rope_kv_write.argtypes = [sp, _i32, _vp, _vp, _vp, ctypes.POINTER(_CRope)] + [_vp] * 10
+        lib.gdn_paged_attention.argtypes = [sp] + [_vp] * 8 + [ctypes.c_float, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]
         lib.gdn_paged_attention_workspace_size.argtypes = [sp]
         lib.gdn_draft_accept.argtypes = [ap] + [_vp] * 13 + [ctypes.c_size_t, _vp, _vp]
         lib.gdn_draft_accept_workspace_size.argtypes = [ap]
@@ -107,8 +104,37 @@ def _library():
 
 
 # ---------------------------------------------------------------- marshalling helpers
-# A small call is bound by this file: a tensor costs about half a microsecond here, so the checks ask for
-# what is cheap to ask for (the device as its index) and leave finding the message to _refuse.
+# A small call is bound by this file, so the tensors' checks are native (csrc/marshal.cpp): _ptr, _opt and _view are
+# the extension's functions from the first call on.
+def _ptr(*args):
+    """Pointer of a contiguous tensor: (tensor, name, dtype, shape, device index)."""
+    _load_marshal()
+    return _ptr(*args)
+
+
+def _opt(*args):
+    """The same, or None for None."""
+    _load_marshal()
+    return _opt(*args)
+
+
+def _view(*args):
+    """A gdn_heads_view, as bytes, of a [C, N, heads, D] tensor whose last dimension is contiguous and whose tokens
+    are evenly strided over the lanes (a slice of a stacked projection, or a contiguous tensor)."""
+    _load_marshal()
+    return _view(*args)
+
+
+def _load_marshal() -> None:
+    global _ptr, _opt, _view
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError("_marshal.so is missing: build it with `python -m gated_deltanet_speculative_amd.build`") from e
+    _marshal.init(_refuse)
+    _ptr, _opt, _view = _marshal.ptr, _marshal.opt, _marshal.view
+
+
 def _refuse(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -123,40 +149,12 @@ def _refuse(t, name, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _ptr(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
-    """Pointer of a contiguous tensor of this type and shape on this device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, device)
-    return t.data_ptr()
-
-
-def _opt(t, name, dtype, shape, device) -> Optional[int]:
-    return None if t is None else _ptr(t, name, dtype, shape, device)
-
-
 def _device(t, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     return t.get_device()
-
-
-def _view(t, name: str, dtype: torch.dtype, sh: AttnShape, heads: int, device: int) -> _CView:
-    """A [C, N, heads, D] tensor whose last dimension is contiguous and whose tokens are evenly
-    strided over the lanes (a slice of a stacked projection, or a contiguous tensor)."""
-    C, N = sh.n_seqs, sh.n_nodes
-    shape = (C, N, heads, sh.head_dim)
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device):
-        _refuse(t, name, dtype, shape, device)
-    s0, s1, s2, s3 = t.stride()
-    if s3 != 1:
-        raise ValueError(f"{name}: values of one head must be contiguous")
-    if N > 1 and C > 1 and s0 != N * s1:
-        raise ValueError(f"{name}: token rows must be evenly strided across lanes")
-    token = s1 if N > 1 else s0 if C > 1 else 0
-    return _CView(t.data_ptr(), token, s2 if heads > 1 else 0)
 
 
 def _status_word(status, device) -> torch.Tensor:
@@ -221,18 +219,18 @@ def rope_kv_write(sh: AttnShape, q, k, v, inv_freq, k_cache, v_cache, slot_ids, 
         q_out = torch.empty((C, N, sh.n_q_heads, D), dtype=sh.dtype, device=device)
     status = _status_word(status, device)
     x = torch.float32 if q.dtype is torch.float32 else sh.dtype
-    views = [_view(t, n, x, sh, heads, device) for t, n, heads in
-             ((q, "q", sh.n_q_heads), (k, "k", sh.n_kv_heads), (v, "v", sh.n_kv_heads))]
+    q_shape, kv_shape = (C, N, sh.n_q_heads, D), (C, N, sh.n_kv_heads, D)
     rope = _CRope(_ptr(inv_freq, "inv_freq", torch.float64, (half,), device),
                   _opt(positions, "positions", torch.int32, (C, N, n_axes), device),
                   _opt(pair_axis, "pair_axis", torch.int32, (half,), device), n_axes, 2 * half, int(bool(interleaved)),
                   _opt(q_norm, "q_norm", torch.float32, (D,), device),
                   _opt(k_norm, "k_norm", torch.float32, (D,), device), eps)
     _call(device, _library().gdn_rope_kv_write, "gdn_rope_kv_write", ctypes.byref(_cs(sh)), _dtype_code(x),
-          *map(ctypes.byref, views), ctypes.byref(rope), _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
+          _view(q, "q", x, q_shape, device), _view(k, "k", x, kv_shape, device), _view(v, "v", x, kv_shape, device),
+          ctypes.byref(rope), _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
           _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *_places(sh, slot_ids, page_table, seq_len, device),
           *_tree(sh, parents, lane_nodes, device),
-          _ptr(q_out, "q_out", sh.dtype, (C, N, sh.n_q_heads, D), device), status.data_ptr())
+          _ptr(q_out, "q_out", sh.dtype, q_shape, device), status.data_ptr())
     return q_out, status
 
 
@@ -262,7 +260,7 @@ def paged_attention(sh: AttnShape, q, k_cache, v_cache, slot_ids, page_table, se
           _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
           _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *_places(sh, slot_ids, page_table, seq_len, device),
           *_tree(sh, parents, lane_nodes, device), 1.0 / math.sqrt(sh.head_dim) if scale is None else scale,
-          None if gate is None else ctypes.byref(_view(gate, "gate", sh.dtype, sh, sh.n_q_heads, device)), int(gate_mode),
+          None if gate is None else _view(gate, "gate", sh.dtype, shape, device), int(gate_mode),
           _ptr(out, "out", sh.dtype, shape, device), workspace.data_ptr(), workspace.numel() * 4, status.data_ptr())
     return out, status
 
@@ -334,7 +332,7 @@ def kv_commit_layers(sh: AttnShape, k_caches, v_caches, slot_ids, page_table, se
         raise ValueError("kv_commit_layers: k_caches and v_caches differ in length")
     if not 1 <= len(ks) <= MAX_LAYERS:
         raise ValueError(f"kv_commit_layers: {len(ks)} layers, expected 1..{MAX_LAYERS}")
-    arr = _vp * len(ks)
+    arr = struct.Struct(f"{len(ks)}P").pack
     _call(device, _library().gdn_kv_commit_layers, "gdn_kv_commit_layers", ctypes.byref(_cs(sh)), len(ks), arr(*ks),
           arr(*vs), *_places(sh, slot_ids, page_table, seq_len, device), *_tree(sh, parents, lane_nodes, device),
           _ptr(accept_node, "accept_node", torch.int32, (sh.n_seqs,), device),

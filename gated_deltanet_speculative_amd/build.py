@@ -3,7 +3,7 @@
     python -m gated_deltanet_speculative_amd.build
 
 Compiles every source under csrc/ to an object in _build/ and links the shared
-library next to this file.  Always recompiles (cheap: a few seconds per file).
+library next to this file, and beside it the binding's tensor checks (_marshal.so, g++).  Always recompiles (cheap: a few seconds per file).
 """
 
 from __future__ import annotations
@@ -18,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdnverify.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = "gfx950"
 
 SOURCES = ["gdn_api.cpp", "conv_tree_step.hip", "tree_verify.hip", "replay_commit.hip", "decode_step.hip",
@@ -57,10 +58,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_marshal() -> str:
+    """The binding's tensor checks as a Python extension (host code only, against torch's headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    includes = [a for d in (*ext.include_paths(), sysconfig.get_paths()["include"]) for a in ("-isystem", d)]
+    libs = [a for d in ext.library_paths() for a in (f"-L{d}", f"-Wl,-rpath,{d}")]
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *includes, os.path.join(CSRC, "marshal.cpp"), "-o", tmp, *libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(_compile, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -6,6 +6,7 @@ import ctypes
 import os
 import re
 import shutil
+import struct
 import subprocess
 
 import numpy as np
@@ -60,7 +61,7 @@ def _rope(sh=None, x_dtype=1, views=None, rope=None, ptrs=None):
     r.update(rope or {})
     a = dict(k=_p(4), v=_p(5), slot=_p(6), table=_p(7), len=_p(8), parents=None, nodes=None, out=_p(9), status=_p(10))
     a.update(ptrs or {})
-    return _round._library().gdn_rope_kv_write(ctypes.byref(sh or _shape()), x_dtype, *[ctypes.byref(_round._CView(*x)) for x in v],
+    return _round._library().gdn_rope_kv_write(ctypes.byref(sh or _shape()), x_dtype, *[struct.pack("Pqq", x[0] or 0, *x[1:]) for x in v],
                                                ctypes.byref(_round._CRope(**r)), *a.values(), None)
 
 
@@ -70,7 +71,7 @@ def _attn(sh=None, scale=0.125, gate=None, mode=0, ws=_p(12), ws_bytes=1 << 30, 
     p = dict(ptrs or {})
     out, status = p.pop("out", out), p.pop("status", status)
     a.update(p)
-    g = None if gate is None else ctypes.byref(_round._CView(*gate))
+    g = None if gate is None else struct.pack("Pqq", gate[0] or 0, *gate[1:])
     return _round._library().gdn_paged_attention(ctypes.byref(sh or _shape()), *a.values(), scale, g, mode, out, ws, ws_bytes, status, None)
 
 
