@@ -4,8 +4,8 @@
 // With the path a_0 < ... < a_m, row L + j takes row L + a_j.  Parents precede children, so
 // a_j >= j, and a row that is written (L + j) is read only by the steps i <= j (a_i >= i): in
 // ascending order, loads of a step before the stores of the same and later ones, the move is safe
-// in place.  Each thread owns a 16-byte column of every row of one (lane, layer, K or V) and
-// kv head: no other thread reads or writes it, so the order within the thread is enough.
+// in place.  A thread owns a 16-byte column of every row of one (lane, layer, K or V) and kv head:
+// no other thread reads or writes it, so the order within the thread is enough.
 //
 // Bound by launch and by dependent reads (slot, length, page id, row): every workgroup checks all lanes itself, as
 // in the replay commit, so one launch decides; its own rows are found and the first of them loaded ahead of the
@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 256;
 
 constexpr int kBatch = 8;  // preflight entries of a thread that are requested together
-constexpr int kAhead = 4;  // moved rows of a thread in flight
+constexpr int kAhead = 8;  // moved rows of a thread in flight
 
 __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers, CacheLayers cl, PagedLanes l,
                                                              const int32_t *__restrict__ accept_node,
@@ -27,8 +27,8 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
     __shared__ int s_word, s_bits;
     __shared__ int s_slot[GDN_MAX_SEQS], s_len[GDN_MAX_SEQS], s_nodes[GDN_MAX_SEQS];  // slot -1: padding or in error
     __shared__ uint32_t s_src[GDN_MAX_NODES], s_dst[GDN_MAX_NODES];                   // cache rows of kv head 0
-    const int tid = threadIdx.x, lane = tid & 63, c = blockIdx.y, side = blockIdx.x;
-    const bool lengths = side == 2 * n_layers;  // the last workgroup of lane 0 writes the lengths
+    const int tid = threadIdx.x, lane = tid & 63, c = blockIdx.y;
+    const bool lengths = blockIdx.x == gridDim.x - 1;  // the last workgroup of lane 0 writes the lengths
     if (lengths && c != 0) return;
 
     // ---- this lane's path, rows and first loads, ahead of the verdict (a bad page is read as page 0)
@@ -56,17 +56,19 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
     }
     if (tid == 0) s_bits = 0;
     lds_barrier();
-    v4i *cache = static_cast<v4i *>(lengths ? nullptr : side < n_layers ? cl.k[side] : cl.v[side - n_layers]);
-    const size_t head = (size_t)d.page.d * row_chunks;  // 16-byte chunks between the heads of a page
-    const int cols = d.Hkv * row_chunks;
-    v4i v[kAhead];
-    auto load = [&](int col, int j0) {
-        const v4i *p = cache + (col / row_chunks) * head + col % row_chunks;
+    // this thread's column: K or V of a layer, kv head, 16 bytes
+    const int cols = d.Hkv * row_chunks, item = blockIdx.x * kThreads + tid, side = item / cols, col = item - side * cols;
+    const bool mine = !lengths && side < 2 * n_layers;
+    v4i *p = nullptr, v[kAhead];
+    if (mine)
+        p = static_cast<v4i *>(side < n_layers ? cl.k[side] : cl.v[side - n_layers]) +
+            (size_t)(col / row_chunks) * d.page.d * row_chunks + col % row_chunks;
+    auto load = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             if (j0 + j < n) v[j] = p[(size_t)s_src[j0 + j] * row_chunks];
     };
-    if (first < n && tid < cols) load(tid, first);
+    if (mine) load(first);
 
     // ---- preflight over every lane
     int bits = slot_preflight<kThreads>(slots, l.slot_ids, d.C, d.P, s_bitmap, &s_word);  // (has barriers)
@@ -81,27 +83,30 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
     }
     if (l.parents) {
         lds_barrier();
-        for (int k0 = tid; k0 < d.C * d.N; k0 += kThreads * kBatch) {
+        // entry k is node k % 32 of lane k / 32
+        const int i = tid & (GDN_MAX_NODES - 1), last = d.C - 1;
+        for (int t0 = tid / GDN_MAX_NODES; t0 < d.C; t0 += kThreads / GDN_MAX_NODES * kBatch) {
             int par[kBatch], pid[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) par[j] = l.parents[min(k0 + j * kThreads, d.C * d.N - 1)];
+            bool has[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int k = min(k0 + j * kThreads, d.C * d.N - 1), t = k / d.N, i = k - t * d.N;
-                const bool has = s_slot[t] != -1 && i < s_nodes[t];
-                pid[j] = has ? l.page_table[(int64_t)s_slot[t] * d.max_pages + d.page((uint32_t)(s_len[t] + i))] : 0;
-                if (has && (par[j] < -1 || par[j] >= i)) bits |= GDN_STATUS_PARENT;
+                const int t = t0 + j * (kThreads / GDN_MAX_NODES), u = min(t, last);
+                has[j] = (t <= last) & (i < d.N) & (s_slot[u] != -1) & (i < s_nodes[u]);
+                par[j] = l.parents[(int64_t)u * d.N + min(i, d.N - 1)];
+                pid[j] = l.page_table[has[j] ? (int64_t)s_slot[u] * d.max_pages + d.page((uint32_t)(s_len[u] + i)) : 0];
             }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if ((unsigned)pid[j] >= (unsigned)d.n_pages) bits |= GDN_STATUS_PAGE;
+            for (int j = 0; j < kBatch; ++j) {
+                if (has[j] & ((par[j] < -1) | (par[j] >= i))) bits |= GDN_STATUS_PARENT;
+                if (has[j] & ((unsigned)pid[j] >= (unsigned)d.n_pages)) bits |= GDN_STATUS_PAGE;
+            }
         }
     }
     if (bits) atomicOr(&s_bits, bits);
     lds_barrier();
     bits = s_bits;
     const bool commit = st_in == 0 && bits == 0;
-    if (bits && tid == 0 && side == 0) atomicOr(l.status, bits);
+    if (bits && tid == 0 && blockIdx.x == 0) atomicOr(l.status, bits);
 
     if (lengths) {
         for (int s = tid; s < d.P; s += kThreads) new_len[s] = l.seq_len[s];
@@ -124,14 +129,12 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
     if (!commit) return;
 
     // ---- the rows behind the first gap, kAhead loads in flight; a row written by a step is read by none behind it
-    for (int col = tid; col < cols; col += kThreads) {
-        v4i *p = cache + (col / row_chunks) * head + col % row_chunks;
-        for (int j0 = first; j0 < n; j0 += kAhead) {
-            if (col != tid || j0 != first) load(col, j0);
+    if (!mine) return;
+    for (int j0 = first; j0 < n; j0 += kAhead) {
+        if (j0 != first) load(j0);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (j0 + j < n) p[(size_t)s_dst[j0 + j] * row_chunks] = v[j];
-        }
+        for (int j = 0; j < kAhead; ++j)
+            if (j0 + j < n) p[(size_t)s_dst[j0 + j] * row_chunks] = v[j];
     }
 }
 
@@ -142,8 +145,10 @@ hipError_t launch_kv_commit(const AttnDims &d, int n_layers, const CacheLayers &
     const int es = d.dtype == GDN_DTYPE_F32 ? 4 : 2;
     // without parents no row moves: only the workgroup that writes the lengths is launched
     const int layers = l.parents ? n_layers : 0;
-    hipLaunchKernelGGL(kv_commit_kernel, dim3(2 * layers + 1, l.parents ? d.C : 1), dim3(kThreads), 0, stream, d, layers,
-                       cl, l, accept_node, new_len, d.D * es / 16);
+    const int row_chunks = d.D * es / 16;
+    const int64_t items = 2ll * layers * d.Hkv * row_chunks;  // columns of a lane, one a thread
+    hipLaunchKernelGGL(kv_commit_kernel, dim3((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1),
+                       dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     return hipGetLastError();
 }
 
