@@ -9,6 +9,7 @@
 //                                             tensor of another type, shape, device or layout, and raises
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -46,8 +47,10 @@ const at::Tensor *checked(PyObject *const *a, Py_ssize_t n, bool contiguous) {
 }
 
 PyObject *ptr(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS  // (a tensor without storage or with symbolic sizes throws)
     const at::Tensor *t = checked(a, n, true);
     return t ? PyLong_FromUnsignedLongLong(reinterpret_cast<uintptr_t>(t->data_ptr())) : nullptr;
+    END_HANDLE_TH_ERRORS
 }
 
 PyObject *opt(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -56,6 +59,7 @@ PyObject *opt(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 PyObject *view(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     const at::Tensor *t = checked(a, n, false);
     if (!t) return nullptr;
     if (t->dim() != 4) {
@@ -74,6 +78,7 @@ PyObject *view(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t v[3] = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(t->data_ptr())),
                           N > 1 ? t->stride(1) : C > 1 ? t->stride(0) : 0, heads > 1 ? t->stride(2) : 0};
     return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(v), sizeof v);
+    END_HANDLE_TH_ERRORS
 }
 
 PyObject *init(PyObject *, PyObject *refuse) {

@@ -225,6 +225,23 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         sh._replace(dtype=torch.int8).c_struct()
 
 
+@built
+def test_binding_survives_tensors_without_storage():
+    """A tensor that only pretends to be on a device raises; the process goes on."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    sh = gdn.AcceptShape(1, 1, 5)
+    with FakeTensorMode():
+        fake = torch.empty(1, 1, 5, device="meta")
+    with pytest.raises((ValueError, TypeError, RuntimeError)):
+        gdn.draft_accept(sh, fake, torch.zeros(1, 1, dtype=torch.int32))
+    for t, shape in ((torch.empty(3, device="meta"), (3,)), (torch.zeros(3).to_sparse(), (3,)), (torch.zeros(3), (4,)), ("no", (3,))):
+        with pytest.raises((ValueError, TypeError)):
+            _round._ptr(t, "t", torch.float32, shape, 0)
+    with pytest.raises(TypeError):
+        _round._ptr(torch.zeros(3), "t", torch.float32)
+
+
 # ---------------------------------------------------------------- pins of the oracle
 def test_oracle_attention_closed_forms():
     """Equal keys average the attended values; one attended row is its value; a tree node is its path's chain."""
