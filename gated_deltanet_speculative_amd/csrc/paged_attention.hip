@@ -74,7 +74,8 @@ struct Type<float> {
 constexpr int tile_rows(int row_bytes) { return row_bytes < 256 ? 64 : 16384 / row_bytes; }
 // A workgroup of the row kernel: its waves, and tiles of 16 query rows per wave, by its query rows.  Two tiles per wave
 // halve the LDS reads per product; rows of 512 bytes and more leave room for one (its outputs and queries alone are
-// 96 registers and more).  Eight waves share a tile's loads and staging registers.
+// 96 registers and more), and so do float32 ones (two lanes of 64 nodes, 4 heads each, D = 64, 88 rows: 40 us with 256
+// query rows, 16 with 128).  Eight waves share a tile's loads and staging registers.
 constexpr int group_waves(int rows) { return rows == 64 ? 4 : 8; }
 constexpr int group_tiles(int rows) { return rows == 256 ? 2 : 1; }
 
@@ -239,7 +240,7 @@ __device__ inline void leave_nothing(const AttnArgs &a, const AttnPlan &plan, in
 // of 4 x 16 nodes behind 8192 tokens 33.8 us, 4.0 TB/s.  256 rows a workgroup instead of 128 took the prompt from 233
 // to 205 us (staging registers and page look-ups shared by twice the rows), operands read four products ahead 205 to 195.
 template <typename T, int D, int BM>
-__global__ __launch_bounds__(64 * group_waves(BM), 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 1 : 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = group_waves(BM), kThreads = 64 * kWaves, RT = group_tiles(BM), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
     static_assert(BM == 16 * RT * kWaves && RPP <= TOK, "");
@@ -1245,15 +1246,15 @@ hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     if constexpr (RB < 1024)
         if (p.rows_per_group == kFewRows)
             hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
-    if constexpr (RB < 512) {
+    if constexpr (RB < 512 || sizeof(T) == 4)
         if (p.rows_per_group == 64) launch_rows<T, D, 64>(a, p, units, stream);
+    if constexpr (RB < 512 && sizeof(T) == 2)
         if (p.rows_per_group == 256) launch_rows<T, D, 256>(a, p, units, stream);
-    }
     if constexpr (D == 256 && sizeof(T) == 2) {
         if (p.rows_per_group == kPairRows)
             hipLaunchKernelGGL((attn_pair_kernel<T>), dim3(p.tiles > 1 ? (units + 7) / 8 * 8 : units), dim3(kPairThreads), 0,
                                stream, a, p);
-    } else {
+    } else if constexpr (RB < 1024) {
         if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
     }
     if (p.splits > 1) {
@@ -1277,11 +1278,20 @@ AttnPlan attn_plan(const AttnDims &d) {
     AttnPlan p;
     const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
     const int64_t rows = (int64_t)d.N * d.G;
-    const bool few = rows <= kFewRows && row_bytes < 1024;
-    p.rows_per_group = few ? kFewRows : row_bytes >= 512 || (rows > 64 && rows <= 128) ? 128 : rows <= 64 ? 64 : 256;
+    const bool few = rows <= kFewRows && row_bytes < 1024, wide = row_bytes >= 512, f32 = d.dtype == GDN_DTYPE_F32;
+    // Wide float32 rows take 64 query rows, four waves of up to 512 registers: within 256, the outputs, queries and
+    // staged rows of a wave do not fit (31 nodes, 4 heads each, D = 256, 136 rows: 52 us with 128 query rows, 28 with
+    // 64; two lanes of 73 nodes at 1.4k 196 and 98).  Rows of 512 bytes do nearly fit, and a long prompt's share of
+    // loads then counts for more (D = 128: 92 query rows 23 us and 18; 5296 of them at 870 rows 245 us and 288).
+    p.rows_per_group = few ? kFewRows
+                       : row_bytes == 1024 || (wide ? f32 && rows <= 128 : rows <= 64) ? 64
+                       : wide || f32 || rows <= 128 ? 128 : 256;
     p.tiles = (int)((rows + p.rows_per_group - 1) / p.rows_per_group);
     const int64_t groups = (int64_t)d.C * d.Hkv * p.tiles;
-    const int64_t least = few ? few_tile(row_bytes) * kFewWaves : 256;  // cache rows of a part
+    // the least cache rows of a part: a short cache is otherwise read by few workgroups, one tile after another (426
+    // nodes, 8 heads, D = 256, 151 rows: 36 us with parts of 256 rows, 32 with 128; float32, 31 nodes at 136: 109 and,
+    // with 64, 52)
+    const int64_t least = few ? few_tile(row_bytes) * kFewWaves : f32 ? 64 : 128;
     const int64_t most = ((int64_t)d.max_pages * d.page.d + least - 1) / least;
     // one round of workgroups: two of them fit a CU (more of them, shorter: tree of 4x16 at 8k 43 us with 512, 52 with
     // 1024; decode of 64 lanes 592 and 581; 5x8 float32 chains at 3k 21.7 and 24.8)
