@@ -328,3 +328,35 @@ def test_absent_pages_in_every_kernel(D, G, N):
         out, res, status, bits = _run(pg, q, table=table)
         assert status == R.PAGE and bits == R.PAGE
         check_attention(out, res, BF, ctx=f"page {at}")
+
+
+@pytest.mark.parametrize("dtype,D,G", [(BF, 64, 2), (HF, 128, 1), (BF, 256, 1), (FP, 64, 1)])
+def test_the_longest_chunk(dtype, D, G):
+    """65536 tokens in one call, behind 77 rows: sampled rows, each as a single token behind those before it."""
+    N, L = 65536, 77
+    pg = Paged(1, N, G, 1, D, 256, dtype, [L], seed=D + G)
+    q = pg.normal(1, N, G, D)
+    out = torch.full((1, N, G, D), SENTINEL, dtype=dtype, device="cuda")
+    ws = torch.empty(max(gdn.paged_attention_workspace_size(pg.sh) // 4, 1), device="cuda")
+    _, status = gdn.paged_attention(pg.sh, q, pg.k, pg.v, *pg.places(), out=out, workspace=ws)
+    assert int(status.item()) == 0
+    k, v = as_numpy(pg.k), as_numpy(pg.v)
+    for i in (0, 1, 127, 255, 256, 5000, 32767, 40001, 65279, 65534, 65535):
+        length = np.where(np.arange(pg.sh.n_slots) == pg.slots[0], L + i, 0).astype(np.int32)
+        res, bits = R.paged_attention(as_numpy(q[:, i:i + 1]), k, v, pg.slots, pg.table, length)
+        assert bits == 0
+        check_attention(out[:, i:i + 1], res, dtype, ctx=f"token {i}")
+
+
+@pytest.mark.parametrize("dtype,D,N", [(BF, 128, 1), (FP, 256, 1), (HF, 256, 5), (FP, 64, 6)])
+def test_the_most_lanes(dtype, D, N):
+    """1024 lanes of every length from 0 to 60, some of them padding, shorter or sharing a page of the prefix."""
+    C = 1024
+    pg = Paged(C, N, 4, 1, D, 16, dtype, [c % 61 for c in range(C)], seed=D + N)
+    slots, nodes = pg.slots.copy(), pg.rng.integers(0, N + 1, C).astype(np.int32)
+    slots[::7] = -1
+    for c in range(20, 1024, 61):  # lanes of 20 rows and more: the first page is full
+        pg.table[pg.slots[c], 0] = pg.table[pg.slots[20], 0]
+    out, res, status, bits = _run(pg, pg.normal(C, N, 4, D), None, nodes, slots=slots)
+    assert status == bits == 0
+    check_attention(out, res, dtype)

@@ -316,6 +316,47 @@ def test_commit_is_a_transaction():
     assert _commit(pg, accept, parents, slots=slots, table=table) == 0
 
 
+def test_write_and_commit_past_32_bits():
+    """Pools of more than 2^32 bytes: rows are written and moved where they lie, as in a small pool."""
+    page, D, Hkv, N, L = 128, 256, 4, 6, 250
+    per = Hkv * page * D * 2
+    n_pages = (1 << 32) // per + 40
+    small = Paged(1, N, 8, Hkv, D, page, BF, [L], seed=21, extra_slots=0, spare_pages=0)
+    sh = small.sh._replace(n_pages=n_pages)
+    ids = np.array([[3, n_pages - 1]], np.int32)
+    k, v = (torch.zeros(sh.cache_shape, dtype=BF, device="cuda") for _ in range(2))
+    for big, of in ((k, small.k), (v, small.v)):
+        for j in range(2):
+            big[int(ids[0, j])] = of[int(small.table[0, j])]
+    q_, k_, v_ = _qkv(small, BF)
+    inv, (slots, table, length) = dev(1e4 ** (-np.arange(64) / 64)), small.places()
+    parents = dev(np.array([[-1, 0, 0, 1, 2, 3]], np.int32))
+    accept = dev(np.array([5], np.int32))  # nodes 0, 1, 3, 5: rows L + 3 and L + 5 move to L + 2 and L + 3
+    for sh_, kk, vv, tab in ((small.sh, small.k, small.v, table), (sh, k, v, dev(ids))):
+        _, status = gdn.rope_kv_write(sh_, q_, k_, v_, inv, kk, vv, slots, tab, length, parents=parents)
+        gdn.kv_commit_layers(sh_, [kk], [vv], slots, tab, length, accept, status, parents=parents)
+        assert int(status.item()) == 0
+    for big, of in ((k, small.k), (v, small.v)):
+        for j in range(2):
+            assert torch.equal(big[int(ids[0, j])], of[int(small.table[0, j])])
+
+
+def test_most_lanes_of_the_write_and_the_commit():
+    C, N = 1024, 7
+    pg = Paged(C, N, 2, 1, 64, 16, BF, [c % 40 for c in range(C)], seed=22)
+    parents, nodes = random_parents(pg.rng, C, N), pg.rng.integers(1, N + 1, C).astype(np.int32)
+    slots = pg.slots.copy()
+    slots[::9] = -1
+    res, bits = _rope(pg, *_qkv(pg, BF), 32, parents, nodes, slots=slots)
+    assert bits == 0 and len(res) == int(nodes[slots >= 0].sum())
+    pg.k, pg.v = pg.k[None].contiguous(), pg.v[None].contiguous()
+    accept = np.minimum(pg.rng.integers(-1, N, C), nodes - 1).astype(np.int32)
+    assert _commit(pg, accept, parents, nodes, slots=slots) == 0
+    again = slots.copy()
+    again[1023] = again[1]  # the last lane and one of the first
+    assert _commit(pg, accept, parents, nodes, slots=again) == R.SLOT_DUP
+
+
 # ---------------------------------------------------------------- a round, as it is used
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("sharp", [1.0, 4.0])
