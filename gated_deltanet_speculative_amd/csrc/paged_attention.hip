@@ -1292,12 +1292,21 @@ AttnPlan attn_plan(const AttnDims &d) {
     // nodes, 8 heads, D = 256, 151 rows: 36 us with parts of 256 rows, 32 with 128; float32, 31 nodes at 136: 109 and,
     // with 64, 52)
     const int64_t least = few ? few_tile(row_bytes) * kFewWaves : f32 ? 64 : 128;
-    const int64_t most = ((int64_t)d.max_pages * d.page.d + least - 1) / least;
-    // one round of workgroups: two of them fit a CU (more of them, shorter: tree of 4x16 at 8k 43 us with 512, 52 with
-    // 1024; decode of 64 lanes 592 and 581; 5x8 float32 chains at 3k 21.7 and 24.8)
-    constexpr int64_t kRound = 512;
-    int64_t s = (kRound + groups - 1) / groups;
-    if (s > most) s = most;
+    const int64_t held = (int64_t)d.max_pages * d.page.d, most = (held + least - 1) / least;
+    // One round of workgroups: one of eight waves, or of four that hold more than 256 registers, fills a CU, two others
+    // do.  Not one more: a round of few costs as much as a full one (rounded up, to 512 in every kernel, against this:
+    // three lanes of 710 nodes, 4 heads each, D = 64: 62 us and 35; 21 nodes of 4, D = 256, six lanes at 19k 289 and
+    // 201; 24 nodes of 8, D = 128, seven lanes at 7.6k 41 and 31).
+    const int64_t round = p.rows_per_group >= 128 || (f32 && p.rows_per_group == 64) ? 256 : 512;
+    auto rounds = [&](int64_t s) { return (groups * s + round - 1) / round; };
+    int64_t s = groups < round ? round / groups : 1;
+    s = s > most ? most : s;
+    // More rounds of shorter parts where they leave the last one fuller, by 15% and more, and the parts are long beside
+    // what writing and joining one costs (42 lanes of 32 nodes, 4 heads each, D = 128, at 11k: 410 us and 364; 2278
+    // nodes of 8 at 2k, D = 256, float32 2000 and 1550; but 710 nodes of D = 64 without the bound of 2048 rows 35 and 62;
+    // float32 products cost eight times as much a row).
+    for (int64_t more = s + 1; (f32 ? 192 : 2048) * more <= held && groups * more <= 4 * round; ++more)
+        if (20 * rounds(more) * s < 17 * rounds(s) * more) s = more;
     p.splits = (int)(s > 64 ? 64 : s);
     return p;
 }
