@@ -14,6 +14,7 @@
 // the accumulators hold them, which the left operand follows); no score goes through memory.
 // The left operand V^T takes four cache rows of one column per lane: the 16-bit path reads it
 // with the transposing LDS load, the 32-bit path with plain loads of one value.
+#include <algorithm>
 #include <type_traits>
 
 #include "round_device.h"
@@ -1292,7 +1293,7 @@ AttnPlan attn_plan(const AttnDims &d) {
     // nodes, 8 heads, D = 256, 151 rows: 36 us with parts of 256 rows, 32 with 128; float32, 31 nodes at 136: 109 and,
     // with 64, 52)
     const int64_t least = few ? few_tile(row_bytes) * kFewWaves : f32 ? 64 : 128;
-    const int64_t held = (int64_t)d.max_pages * d.page.d, most = (held + least - 1) / least;
+    const int64_t held = (int64_t)d.max_pages * d.page.d, most = std::min<int64_t>((held + least - 1) / least, 64);
     // One round of workgroups: one of eight waves, or of four that hold more than 256 registers, fills a CU, two others
     // do.  Not one more: a round of few costs as much as a full one (rounded up, to 512 in every kernel, against this:
     // three lanes of 710 nodes, 4 heads each, D = 64: 62 us and 35; 21 nodes of 4, D = 256, six lanes at 19k 289 and
@@ -1305,9 +1306,9 @@ AttnPlan attn_plan(const AttnDims &d) {
     // what writing and joining one costs (42 lanes of 32 nodes, 4 heads each, D = 128, at 11k: 410 us and 364; 2278
     // nodes of 8 at 2k, D = 256, float32 2000 and 1550; but 710 nodes of D = 64 without the bound of 2048 rows 35 and 62;
     // float32 products cost eight times as much a row).
-    for (int64_t more = s + 1; (f32 ? 192 : 2048) * more <= held && groups * more <= 4 * round; ++more)
+    for (int64_t more = s + 1; more <= most && (f32 ? 192 : 2048) * more <= held && groups * more <= 4 * round; ++more)
         if (20 * rounds(more) * s < 17 * rounds(s) * more) s = more;
-    p.splits = (int)(s > 64 ? 64 : s);
+    p.splits = (int)s;
     return p;
 }
 
