@@ -360,3 +360,17 @@ def test_the_most_lanes(dtype, D, N):
     out, res, status, bits = _run(pg, pg.normal(C, N, 4, D), None, nodes, slots=slots)
     assert status == bits == 0
     check_attention(out, res, dtype)
+
+
+@pytest.mark.parametrize("dtype,N", [(FP, 6), (BF, 17), (HF, 17)])
+def test_more_workgroups_than_a_round_with_the_cache_split(dtype, N):
+    """260 groups of rows, two or three parts each, most of them behind a lane's last row."""
+    C = 65
+    pg = Paged(C, N, 16, 4, 64, 32, dtype, [(37 * c) % 601 for c in range(C)], seed=N)
+    pg.table = np.pad(pg.table, ((0, 0), (0, 160 - pg.table.shape[1])), constant_values=-1)
+    pg.sh = pg.sh._replace(max_pages=160)
+    nodes = pg.rng.integers(0, N + 1, C).astype(np.int32)
+    assert gdn.paged_attention_workspace_size(pg.sh) > 0
+    out, res, status, bits = _run(pg, pg.normal(C, N, 16, 64), random_parents(pg.rng, C, N), nodes)
+    assert status == bits == 0
+    check_attention(out, res, dtype)
