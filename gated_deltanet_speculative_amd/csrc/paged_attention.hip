@@ -33,11 +33,19 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 // ---- the value types: 16-byte operand fragments and the matrix instructions on them.
 // A fragment holds 64 bytes' worth of one row over the four lane groups: 32 16-bit or 16 32-bit
 // contraction indices per step.
+// 16-bit weights are rounded to their type for the second product (the 16-bit matrix instructions take no others,
+// and two of them, for a weight in two parts, would double that product); the sum keeps them in 32 bits.  kLift: how
+// many powers of two the exponentials' base lies below the running maximum.  float16 holds numbers below 2^-14 with
+// a fixed error of 2^-25: with a base at the maximum, weights 15 powers of two and more below it would lose their
+// last bits and those 25 below it vanish, while the sum counts them (one row 16 nats above 262144 equal ones: the output is
+// 6% off).  Nine powers lower the largest weight is 2^(9 + kSlack) = 2^15, inside the type's range, and a row's
+// weight is off by half a step or by 2^-34 of the largest one.  Costs nothing: the base is one number a row.
 template <typename T>
 struct Type;
 template <>
 struct Type<__bf16> {
     static constexpr unsigned kExp = 0x7f80u, kOne = 0x3f80u;
+    static constexpr float kLift = 0.f;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     }
@@ -53,6 +61,7 @@ struct Type<__bf16> {
 template <>
 struct Type<_Float16> {
     static constexpr unsigned kExp = 0x7c00u, kOne = 0x3c00u;
+    static constexpr float kLift = 9.f;
     static __device__ v4f mma(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
     }
@@ -68,8 +77,13 @@ struct Type<_Float16> {
 template <>
 struct Type<float> {
     static constexpr unsigned kExp = 0x7f800000u, kOne = 0x3f800000u;
+    static constexpr float kLift = 0.f;
     static __device__ v4f mma(v4i a, v4i b, v4f c) { return mfma4(__builtin_bit_cast(v4f, a), __builtin_bit_cast(v4f, b), c); }
 };
+
+// Base of the exponentials for a running maximum (nothing attended yet: any, every weight is 2^-inf)
+template <typename T>
+__device__ inline float weight_base(float m) { return (m == kNegInf ? 0.f : m) - Type<T>::kLift; }
 
 // Cache rows of a tile: 16 KiB of K and as much of V, at most 64 rows (a set of them is 64 bits).
 constexpr int tile_rows(int row_bytes) { return row_bytes < 256 ? 64 : 16384 / row_bytes; }
@@ -419,7 +433,7 @@ __global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 
         }
         float base[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) base[rt] = m[rt] == kNegInf ? 0.f : m[rt];  // nothing attended yet: every weight is 2^-inf
+        for (int rt = 0; rt < RT; ++rt) base[rt] = weight_base<T>(m[rt]);
         auto weigh = [&](int rt, int e) {  // score e of this lane becomes its weight
             const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][e >> 2][e & 3], a.scale_log2, -base[rt]));
             s[rt][e >> 2][e & 3] = x;
@@ -778,7 +792,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, 
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float base = m[rt] == kNegInf ? 0.f : m[rt];
+                const float base = weight_base<T>(m[rt]);
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
@@ -1033,7 +1047,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) o[dt] *= shrink;
         }
-        const float base = m == kNegInf ? 0.f : m;
+        const float base = weight_base<T>(m);
         float sum = 0.f;
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)

@@ -30,7 +30,8 @@
  *     value buffers are 16-byte aligned, int32 buffers 4-byte, inv_freq 8-byte aligned;
  *   - softmax statistics, norms and products are held in 32 bits, angles and the acceptance
  *     tests in 64; a 16-bit path rounds the softmax weights to its type before the product
- *     with v, and every output once;
+ *     with v (half a step each; in float16 at least 2^-34 of a row's largest weight), and every
+ *     output once;
  *   - lanes of one call use different slots (SLOT_DUP in the calls that write a cache);
  *   - pages that hold rows at or behind a slot's committed length belong to that slot alone
  *     (full pages in front of it may be shared between slots).

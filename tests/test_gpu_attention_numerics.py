@@ -1,0 +1,64 @@
+"""Attention over the paged cache where its arithmetic is strained, in every kernel: weights many powers of two
+below the largest one."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_speculative_amd as gdn
+from gpu_util import log
+from oracle import round_oracle as R
+from round_util import SENTINEL, Paged, as_numpy, attention_tolerance, dev
+
+pytestmark = pytest.mark.gpu
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+# Head layouts that reach every kernel with 8 nodes: few rows, 64, 128 and 256 rows a workgroup, pairs of waves, each type
+KERNELS = [(64, 2), (64, 8), (64, 16), (64, 40), (128, 2), (128, 8), (128, 16), (128, 40), (256, 1), (256, 2), (256, 40)]
+
+
+def _rows(pg, c, n):
+    """(page, place) of the first n rows of lane c's cache."""
+    t = np.arange(n)
+    return pg.table[pg.slots[c], t // pg.sh.page_size].astype(np.int64), t % pg.sh.page_size
+
+
+def _attend(pg, q, **kw):
+    out = torch.full(tuple(q.shape), SENTINEL, dtype=pg.sh.dtype, device="cuda")
+    table = kw.pop("table", pg.table)
+    ws = torch.full((max(gdn.paged_attention_workspace_size(pg.sh) // 4, 1),), float("nan"), device="cuda")
+    _, status = gdn.paged_attention(pg.sh, q, pg.k, pg.v, dev(pg.slots), dev(table), dev(pg.len), out=out, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    return out, int(status.item())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+def test_small_weights_beside_a_large_one(dtype, D, G):
+    """Every 64th row outscores the others, which are equal, by 18 to 24 powers of two and has a value of zero: the
+    output is what the small weights leave, and their rounding is the same for all of them.
+
+    In float16 a weight below 2^-14 is off by up to 2^-25.  The largest weight of a row, and so the sum, is at least
+    2^9, the exponentials' base lying 9 powers of two below a running maximum: each row adds up to 2^-34 |v|."""
+    C, N, lens = 2, 8, [1000, 700]
+    pg = Paged(C, N, G, 1, D, 48, dtype, lens, seed=D + G)
+    k, v = as_numpy(pg.k), np.empty(pg.sh.cache_shape, np.float32)
+    v[:] = pg.rng.uniform(1.0, 2.0, v.shape)
+    k[..., 0] = 0.0
+    for c in range(C):
+        pid, at = _rows(pg, c, lens[c])
+        k[pid[::64], 0, at[::64], 0] = 16.0
+        v[pid[::64], 0, at[::64]] = 0.0
+    pg.k, pg.v = dev(k, dtype), dev(v, dtype)
+    q = np.zeros((C, N, G, D), np.float32)
+    q[..., 0] = pg.rng.integers(48, 65, (C, N, G)) / 64.0
+    q = dev(q, dtype)
+    scale = 24.0 / (16.0 * 1.4426950408889634)
+    log(f"[attn small weights] {dtype} D={D} G={G}")
+    out, status = _attend(pg, q, scale=scale)
+    res, bits = R.paged_attention(as_numpy(q), as_numpy(pg.k), as_numpy(pg.v), pg.slots, pg.table, pg.len, scale=scale)
+    assert status == bits == 0
+    got = as_numpy(out).astype(np.float64)
+    for (c, i), (want, mag, big, rows) in res.items():
+        tol = attention_tolerance(dtype, D, mag, want, big, rows, False) + (rows * 2.0 ** -34 * 2.0 if dtype == HF else 0.0)
+        err = np.abs(got[c, i] - want)
+        assert (err <= tol).all(), f"row {(c, i)}: {float(np.max(err / tol)):.2f} of the tolerance, {float(np.max(err / want)):.2e} relative"
