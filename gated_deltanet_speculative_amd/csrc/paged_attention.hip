@@ -588,7 +588,7 @@ __global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
             v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o[rt][dt] * inv;
-            if (a.gate.p) {
+            if (a.gate.p && sum != 0.f) {  // (zeros where nothing was attended, whatever the gate)
                 const v4f zz = load4(z + 16 * dt + 4 * g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = gated(v[i], zz[i], a.gate_mode);
@@ -908,7 +908,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, 
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
             v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o[rt][dt] * inv;
-            if (a.gate.p) {
+            if (a.gate.p && sum != 0.f) {  // (zeros where nothing was attended, whatever the gate)
                 const v4f zz = load4(z + 16 * dt + 4 * g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = gated(v[i], zz[i], a.gate_mode);
@@ -1184,7 +1184,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
         const int tk = row / d.G, hd = h * d.G + row - tk * d.G;
         const int64_t nd = (int64_t)c * d.N + tk;
         v4f v = sum == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : acc / sum;
-        if (a.gate.p) {
+        if (a.gate.p && sum != 0.f) {
             const v4f z = load4(static_cast<const T *>(a.gate.p) + nd * a.gate.token + hd * a.gate.head + 4 * col);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = gated(v[i], z[i], a.gate_mode);
@@ -1237,7 +1237,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, 
     const int token = r / d.G, head = h * d.G + r - token * d.G;
     const int64_t node = (int64_t)c * d.N + token;
     acc = sum == 0.f ? vw(0.f) : acc / sum;
-    if (a.gate.p) {
+    if (a.gate.p && sum != 0.f) {
         const tw z = *reinterpret_cast<const tw *>(static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head + lane * W);
 #pragma unroll
         for (int i = 0; i < W; ++i) acc[i] = gated(acc[i], (float)z[i], a.gate_mode);

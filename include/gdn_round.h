@@ -131,7 +131,7 @@ int gdn_rope_kv_write(const gdn_attn_shape *sh, int32_t x_dtype, const gdn_heads
  * with act = silu (gate_mode 0) or sigmoid (gate_mode 1) as in gdn_prefill.  A row that a
  * node does not attend to contributes nothing, whatever it holds (NaN and infinities
  * included).  A row in a page outside the pool counts as not attended (PAGE); a node without
- * any attended row of a score above -infinity gets zeros.
+ * any attended row of a score above -infinity gets zeros, whatever its gate holds.
  *
  *   q           [C][N][H_q][D]   (read)
  *   k_cache, v_cache  [n_pages][H_kv][page_size][D]   (read); the round's rows are there

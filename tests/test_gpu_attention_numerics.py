@@ -1,5 +1,5 @@
 """Attention over the paged cache where its arithmetic is strained, in every kernel: weights many powers of two
-below the largest one."""
+below the largest one, rows without anything to attend to behind a gate."""
 
 import numpy as np
 import pytest
@@ -62,3 +62,20 @@ def test_small_weights_beside_a_large_one(dtype, D, G):
         tol = attention_tolerance(dtype, D, mag, want, big, rows, False) + (rows * 2.0 ** -34 * 2.0 if dtype == HF else 0.0)
         err = np.abs(got[c, i] - want)
         assert (err <= tol).all(), f"row {(c, i)}: {float(np.max(err / tol)):.2f} of the tolerance, {float(np.max(err / want)):.2e} relative"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+@pytest.mark.parametrize("mode", [0, 1])
+def test_rows_without_anything_attended_are_zero_behind_any_gate(dtype, D, G, mode):
+    """No page in the pool, or every score minus infinity: zeros, whatever the gate holds."""
+    C, N = 2, 8
+    pg = Paged(C, N, G, 1, D, 48, dtype, [700, 3], seed=D + G)
+    q = dev(pg.rng.uniform(0.5, 1.0, (C, N, G, D)).astype(np.float32), dtype)
+    gate = torch.tensor([float("nan"), float("inf"), -float("inf"), 1.0], device="cuda").to(dtype).repeat(C, N, G, D // 4)
+    log(f"[attn gate of nothing] {dtype} D={D} G={G} mode={mode}")
+    out, status = _attend(pg, q, gate=gate, gate_mode=mode, table=np.full_like(pg.table, -1))
+    assert status == R.PAGE and (as_numpy(out) == 0).all()
+    pg.k.fill_(-float("inf"))
+    out, status = _attend(pg, q, gate=gate, gate_mode=mode)
+    assert status == 0 and (as_numpy(out) == 0).all()
