@@ -27,6 +27,7 @@ constexpr float kNegInf = -__builtin_inff();
 // memory, not the LDS reads and products themselves, whose order is the reading ahead.
 constexpr int kArithmetic = 0x2 | 0x4 | 0x10 | 0x400;
 constexpr float kSlack = 6.f;  // how far, in powers of two, a running maximum may lead its base
+constexpr float kFar = 1048576.f;  // bases beyond this: scores as differences first (from_maximum)
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 
@@ -84,6 +85,26 @@ struct Type<float> {
 // Base of the exponentials for a running maximum (nothing attended yet: any, every weight is 2^-inf)
 template <typename T>
 __device__ inline float weight_base(float m) { return (m == kNegInf ? 0.f : m) - Type<T>::kLift; }
+
+// The exponent of a weight is scale * score - base in one operation, exact but for one rounding, while base is a product
+// that has been rounded: the remainder of the largest score is up to 2^-25 of the base.  Beyond a base of 2^32 that
+// is a weight of 2^128 or of 0.  So far out the product is rounded as the maximum's was (never fused: the largest
+// one's remainder is 0) and the difference taken before the base is: scores become exponents, against the base
+// that is returned.  A wave takes this way for a tile where one of its rows' bases is beyond kFar, where a rounded product
+// is off by at most 2^-4, no more than the sum of a score in 32 bits.
+template <typename T, int N>
+__device__ inline float from_maximum(v4f (&s)[N], float m, float scale) {
+#pragma clang fp contract(off)
+    const float top = m == kNegInf ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = s[k][i] * scale;
+            s[k][i] = x - top;
+        }
+    return -Type<T>::kLift;
+}
 
 // Cache rows of a tile: 16 KiB of K and as much of V, at most 64 rows (a set of them is 64 bits).
 constexpr int tile_rows(int row_bytes) { return row_bytes < 256 ? 64 : 16384 / row_bytes; }
@@ -431,11 +452,20 @@ __global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 
                 for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
             }
         }
-        float base[RT];
+        float base[RT], scale = a.scale_log2;
+        bool far = false;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) base[rt] = weight_base<T>(m[rt]);
+        for (int rt = 0; rt < RT; ++rt) {
+            base[rt] = weight_base<T>(m[rt]);
+            far |= fabsf(base[rt]) > kFar;
+        }
+        if (__builtin_amdgcn_ballot_w64(far)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) base[rt] = from_maximum<T>(s[rt], m[rt], scale);
+            scale = 1.f;
+        }
         auto weigh = [&](int rt, int e) {  // score e of this lane becomes its weight
-            const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][e >> 2][e & 3], a.scale_log2, -base[rt]));
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][e >> 2][e & 3], scale, -base[rt]));
             s[rt][e >> 2][e & 3] = x;
             l[rt] += x;
         };
@@ -790,14 +820,25 @@ __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, 
                     for (int dt = 0; dt < ND; ++dt) o[rt][dt] *= shrink;
                 }
             }
+            float base[RT], scale = a.scale_log2;
+            bool far = false;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float base = weight_base<T>(m[rt]);
+                base[rt] = weight_base<T>(m[rt]);
+                far |= fabsf(base[rt]) > kFar;
+            }
+            if (__builtin_amdgcn_ballot_w64(far)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) base[rt] = from_maximum<T>(s[rt], m[rt], scale);
+                scale = 1.f;
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], a.scale_log2, -base));
+                        const float x = __builtin_amdgcn_exp2f(fmaf(s[rt][tt][i], scale, -base[rt]));
                         s[rt][tt][i] = x;
                         l[rt] += x;
                     }
@@ -1047,13 +1088,17 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a,
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) o[dt] *= shrink;
         }
-        const float base = weight_base<T>(m);
+        float base = weight_base<T>(m), scale = a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(fabsf(base) > kFar)) {
+            base = from_maximum<T>(s, m, scale);
+            scale = 1.f;
+        }
         float sum = 0.f;
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[tt][i] = __builtin_amdgcn_exp2f(fmaf(s[tt][i], a.scale_log2, -base));
+                s[tt][i] = __builtin_amdgcn_exp2f(fmaf(s[tt][i], scale, -base));
                 sum += s[tt][i];
             }
         l += sum;

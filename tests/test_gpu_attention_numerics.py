@@ -1,5 +1,5 @@
 """Attention over the paged cache where its arithmetic is strained, in every kernel: weights many powers of two
-below the largest one, rows without anything to attend to behind a gate."""
+below the largest one, rows without anything to attend to behind a gate, scores of any size."""
 
 import numpy as np
 import pytest
@@ -79,3 +79,59 @@ def test_rows_without_anything_attended_are_zero_behind_any_gate(dtype, D, G, mo
     pg.k.fill_(-float("inf"))
     out, status = _attend(pg, q, gate=gate, gate_mode=mode)
     assert status == 0 and (as_numpy(out) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(dtype, D, G, sign):
+    """Scores of 2^33 and more, far apart: the row of the largest one weighs 1, every other one nothing, so the output
+    is its value, exactly."""
+    C, N, lens = 2, 8, [500, 130]
+    pg = Paged(C, N, G, 1, D, 48, dtype, lens, seed=D + G)
+    k = as_numpy(pg.k)
+    size = np.zeros((C, max(lens) + N))
+    for c in range(C):
+        n = lens[c] + N
+        # distinct values: consecutive float16 ones from 16 on (a 2^-11th apart), bfloat16 ones from 1 on (a 2^-8th)
+        order = pg.rng.permutation(n)
+        bits = (0x4C00 if dtype == HF else 0x3F80) + order.astype(np.uint16)
+        size[c, :n] = sign * (bits.view(np.float16) if dtype == HF else (bits.astype(np.uint32) << 16).view(np.float32))
+        pid, at = _rows(pg, c, n)
+        k[pid, 0, at, 0] = size[c, :n]
+    pg.k = dev(k, dtype)
+    q = np.zeros((C, N, G, D), np.float32)
+    q[..., 0] = np.where(np.arange(G) % 2 == 0, 1.0, 0.75) * (60000.0 if dtype == HF else 1e18)
+    log(f"[attn large scores] {dtype} D={D} G={G} sign={sign}")
+    out, status = _attend(pg, dev(q, dtype), scale=8192.0 if dtype == HF else 0.3)
+    assert status == 0
+    got, v = as_numpy(out), as_numpy(pg.v)
+    for c in range(C):
+        for i in range(N):
+            best = int(np.argmax(size[c, :lens[c] + i + 1]))
+            pid, at = _rows(pg, c, best + 1)
+            assert np.array_equal(got[c, i], np.broadcast_to(v[pid[-1], 0, at[-1]], (G, D))), f"row {(c, i)}: {got[c, i, 0, :4]}"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+def test_equal_scores_of_any_size(dtype, D, G):
+    """Keys that are all the same: the mean of the attended values, at scores of 2^10 to 2^37 of either sign (some rows of a
+    wave beyond the size at which its scores become differences, others not)."""
+    C, N, lens = 2, 8, [500, 130]
+    pg = Paged(C, N, G, 1, D, 48, dtype, lens, seed=D + G)
+    k = as_numpy(pg.k)
+    k[..., 0] = 16.0
+    pg.k = dev(k, dtype)
+    q = np.zeros((C, N, G, D), np.float32)
+    q[..., 0] = pg.rng.choice([-1, 1], (C, N, G)) * 2.0 ** pg.rng.integers(-6, 7, (C, N, G)) * pg.rng.integers(128, 256, (C, N, G)) / 128
+    q = dev(q, dtype)
+    res, _ = R.paged_attention(np.zeros_like(as_numpy(q)), k, as_numpy(pg.v), pg.slots, pg.table, pg.len)
+    for scale in (2.0 ** 12, 2.0 ** 15, 3.0 * 2.0 ** 18, 1.7 * 2.0 ** 24):
+        out, status = _attend(pg, q, scale=scale)
+        assert status == 0
+        got = as_numpy(out).astype(np.float64)
+        for (c, i), (want, mag, _, rows) in res.items():
+            tol = attention_tolerance(dtype, D, mag, want, 0.0, rows, False)
+            err = np.abs(got[c, i] - want)
+            assert (err <= tol).all(), f"scale {scale}, row {(c, i)}: {float(np.max(err / tol)):.2f} of the tolerance"
