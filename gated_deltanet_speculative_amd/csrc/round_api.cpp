@@ -149,7 +149,8 @@ int gdn_paged_attention(const gdn_attn_shape *sh, const void *q, const void *k_c
     if (int r = check_attn(sh, parents != nullptr, &d)) return r;
     if (!q || !k_cache || !v_cache || !slot_ids || !page_table || !seq_len || !out || (gate && !gate->p))
         return GDN_ERR_NULL;
-    if (!(scale > 0.f) || !std::isfinite(scale) || (gate_mode != 0 && gate_mode != 1)) return GDN_ERR_SHAPE;
+    const float scale_log2 = scale * 1.4426950408889634f;  // the kernels' exponentials are of base 2
+    if (!(scale_log2 > 0.f) || !std::isfinite(scale_log2) || (gate_mode != 0 && gate_mode != 1)) return GDN_ERR_SHAPE;
     size_t gb = 0;
     if (gate)
         if (int r = check_view(*gate, d, d.Hq, d.dtype, &gb)) return r;
@@ -171,7 +172,7 @@ int gdn_paged_attention(const gdn_attn_shape *sh, const void *q, const void *k_c
     a.q = q;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     if (gate) a.gate = view_of(*gate);
     a.gate_mode = gate_mode;
     a.out = out;

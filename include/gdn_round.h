@@ -136,7 +136,7 @@ int gdn_rope_kv_write(const gdn_attn_shape *sh, int32_t x_dtype, const gdn_heads
  *   q           [C][N][H_q][D]   (read)
  *   k_cache, v_cache  [n_pages][H_kv][page_size][D]   (read); the round's rows are there
  *   slot_ids, page_table, seq_len, parents, lane_nodes   as above (lanes may share a slot)
- *   scale       > 0 and finite (GDN_ERR_SHAPE)
+ *   scale       > 0, and scale * log2(e) finite (GDN_ERR_SHAPE)
  *   gate        view with H_q heads of the shape's dtype, or NULL   (read)
  *   gate_mode   0 or 1 (GDN_ERR_SHAPE)
  *   out         [C][N][H_q][D]   written for present nodes of valid lanes
