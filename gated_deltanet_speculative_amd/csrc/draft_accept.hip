@@ -369,7 +369,9 @@ __global__ __launch_bounds__(kThreads) void accept_draw_kernel(AcceptArgs a, int
     if (tid == 0) a.next_token[c] = token;
 }
 
-// A (value, index) pair of which the larger value, then the lower index, wins
+// A (value, index) pair of which the larger value, then the lower index, wins.  A NaN stands as -inf with the bit
+// kNan in its index, behind every index of a row: below a value that is -inf.
+constexpr int kNan = 1 << 30;
 struct Best {
     float v;
     int x;
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(kThreads) void accept_best_kernel(AcceptArgs a) {
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (x + e < a.V) b = better(b, Best{v[e] == v[e] ? v[e] : -__builtin_inff(), x + e});
+            if (x + e < a.V) b = better(b, v[e] == v[e] ? Best{v[e], x + e} : Best{-__builtin_inff(), (x + e) | kNan});
     }
     b = wave_best(b);
     if ((tid & 63) == 0) s_best[tid >> 6] = b;
@@ -431,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void accept_walk_kernel(AcceptArgs a, int
         Best b{-__builtin_inff(), 0x7fffffff};
         for (int k = lane; k < chunks; k += 64) b = better(b, all[(size_t)i * chunks + k]);
         b = wave_best(b);
-        if (lane == 0) s_best[i] = b.x;
+        if (lane == 0) s_best[i] = b.x & (kNan - 1);
     }
     __syncthreads();
     if (tid >= 64) return;

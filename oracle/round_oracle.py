@@ -148,6 +148,12 @@ def draw(w, u):
     return int(over[0]) if len(over) else int(np.nonzero(w)[0][-1])
 
 
+def largest(row):
+    """Index of the largest value, the lowest of equal ones; NaN below all, minus infinity among them."""
+    known = np.nonzero(~np.isnan(row))[0]
+    return int(known[np.argmax(row[known])]) if len(known) else 0
+
+
 def draft_accept(target, tokens, root=None, draft=None, parents=None, lane_nodes=None, slot_ids=None, u_accept=None,
                  u_next=None):
     """Returns ({c: (accept_node, n_accept, next_token)}, status)."""
@@ -172,7 +178,7 @@ def draft_accept(target, tokens, root=None, draft=None, parents=None, lane_nodes
         while True:
             row = target[c, node] if node >= 0 else None if root is None else root[c]
             p = None if row is None else np.where(row.astype(np.float64) > 0, row.astype(np.float64), 0.0)
-            best = None if row is None else int(np.argmax(np.where(np.isnan(row), -np.inf, row.astype(np.float64))))
+            best = None if row is None else largest(row)
             refused, went, left = [], None, 1.0
             kids = [j for j in range(n) if par[j] == node]
             for j in kids:
