@@ -1,14 +1,48 @@
-"""The acceptance on the device: the order of rows that hold NaN and infinities."""
+"""The acceptance on the device: its distribution integrated exactly over the random numbers, and the order of rows that
+hold NaN and infinities."""
 
 import numpy as np
 import pytest
 import torch
 
+import acceptance_util as A
 import gated_deltanet_speculative_amd as gdn
+from gpu_util import log
 from round_util import dev
 
 pytestmark = pytest.mark.gpu
 BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+
+
+def _results(case, dtype):
+    """(accept_node, n_accept, next_token) of every lane; every probability is exact in each type."""
+    out = []
+    g = lambda a, t=None: None if a is None else dev(a, t)  # noqa: E731
+    for b in case.blocks(1024):
+        C, N, V = b["target"].shape
+        *got, status = gdn.draft_accept(gdn.AcceptShape(C, N, V, dtype), g(b["target"], dtype), g(b["tokens"]),
+                                        root_target=g(b["root"], dtype), draft=g(b["draft"], dtype), parents=g(b["parents"]),
+                                        u_accept=g(b["u"]), u_next=g(b["u_next"]))
+        assert int(status.item()) == 0
+        out.append(np.stack([t.cpu().numpy() for t in got], 1))
+    return np.concatenate(out)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF, HF])
+def test_candidates_leave_the_targets_distribution(dtype):
+    for cand, case in A.siblings():
+        share = A.share_of_siblings(cand, case, _results(case, dtype))
+        log(f"[accept] candidates {cand}, {case.C} lanes: {share.tolist()}")
+        assert np.abs(share - A.P).max() < 1e-10, cand
+
+
+@pytest.mark.parametrize("dtype", [FP, BF, HF])
+def test_drawn_drafts_leave_the_targets_distribution(dtype):
+    share = sum(A.share_of_drawn(t, case, _results(case, dtype)) for t, case in A.drawn())
+    assert np.abs(share - A.P).max() < 1e-10
+    first, second = (sum(s) for s in zip(*(A.shares_of_chain(p, case, _results(case, dtype)) for p, case in A.drawn_chain())))
+    log(f"[accept] drawn {share.tolist()}, chain {first.tolist()} {(second / second.sum()).tolist()}")
+    assert np.abs(first - A.P).max() < 1e-10 and np.abs(second / second.sum() - A.P2).max() < 1e-10
 
 
 @pytest.mark.parametrize("dtype", [FP, BF, HF])
