@@ -1,9 +1,11 @@
 """Build libgdnverify.so (the C-ABI library) for gfx950 with hipcc, in-tree.
 
-    python -m gated_deltanet_speculative_amd.build
+    python -m gated_deltanet_speculative_amd.build [--library]
 
 Compiles every source under csrc/ to an object in _build/ and links the shared
-library next to this file, and beside it the binding's tensor checks (_marshal.so, g++).  Always recompiles (cheap: a few seconds per file).
+library next to this file, and beside it the Python binding's tensor checks (_marshal.so),
+unless --library is given.  Always recompiles (cheap: a few seconds per file).  The library
+needs hipcc alone; the tensor checks need g++ and the headers of Python and torch.
 """
 
 from __future__ import annotations
@@ -77,23 +79,32 @@ def _build_marshal() -> str:
     return MARSHAL
 
 
-def build(verbose: bool = True) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
-        marshal = ex.submit(_build_marshal)
-        objs = list(ex.map(_compile, SOURCES))
-        marshal.result()
+def _link(objs: list) -> None:
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(verbose: bool = True, binding: bool = True) -> str:
+    """Builds the library and, with `binding`, the tensor checks; the library is there before a failure of the
+    latter is raised."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        marshal = ex.submit(_build_marshal) if binding else None
+        _link(list(ex.map(_compile, SOURCES)))
     if verbose:
         print(f"built {LIB}")
+    if marshal:
+        try:
+            marshal.result()
+        except Exception as e:
+            raise RuntimeError(f"{LIB} is built, the Python binding's {os.path.basename(MARSHAL)} is not: {e}") from e
     return LIB
 
 
 if __name__ == "__main__":
-    build()
+    build(binding="--library" not in sys.argv[1:])
     sys.exit(0)
