@@ -130,8 +130,10 @@ int gdn_rope_kv_write(const gdn_attn_shape *sh, int32_t x_dtype, const gdn_heads
  *   out[c][i][h] = sum_t softmax_t(scale * q[c][i][h] . K[t][h / G]) V[t][h / G]  (* act(gate))
  * with act = silu (gate_mode 0) or sigmoid (gate_mode 1) as in gdn_prefill.  A row that a
  * node does not attend to contributes nothing, whatever it holds (NaN and infinities
- * included).  A row in a page outside the pool counts as not attended (PAGE); a node without
- * any attended row of a score above -infinity gets zeros, whatever its gate holds.
+ * included); an infinite or NaN value of an attended row, of a weight above 2^-34 of the
+ * largest, makes its column of the output infinite or NaN.  A row in a page outside the pool
+ * counts as not attended (PAGE); a node without any attended row of a score above -infinity
+ * gets zeros, whatever its gate holds.
  *
  *   q           [C][N][H_q][D]   (read)
  *   k_cache, v_cache  [n_pages][H_kv][page_size][D]   (read); the round's rows are there

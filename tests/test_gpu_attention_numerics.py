@@ -135,3 +135,23 @@ def test_equal_scores_of_any_size(dtype, D, G):
             tol = attention_tolerance(dtype, D, mag, want, 0.0, rows, False)
             err = np.abs(got[c, i] - want)
             assert (err <= tol).all(), f"scale {scale}, row {(c, i)}: {float(np.max(err / tol)):.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D,G", KERNELS)
+def test_infinite_values_of_committed_rows(dtype, D, G):
+    """An infinity in a row that every node attends to, in a tile without a mask, reaches every node in its column."""
+    C, N, lens = 2, 8, [500, 300]
+    pg = Paged(C, N, G, 1, D, 48, dtype, lens, seed=D + G)
+    q = pg.normal(C, N, G, D)
+    clean = as_numpy(_attend(pg, q)[0])
+    for c in range(C):
+        pid, at = _rows(pg, c, lens[c])
+        pg.v[int(pid[200]), 0, int(at[200]), 7] = float("inf")
+        pg.v[int(pid[1]), 0, int(at[1]), D - 1] = -float("inf")
+        pg.v[int(pid[90]), 0, int(at[90]), 30] = float("nan")
+    got = as_numpy(_attend(pg, q)[0]).copy()
+    assert np.isposinf(got[..., 7]).all() and np.isneginf(got[..., D - 1]).all() and np.isnan(got[..., 30]).all()
+    for col in (7, D - 1, 30):
+        got[..., col] = clean[..., col]
+    assert np.array_equal(got, clean)

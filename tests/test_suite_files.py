@@ -8,7 +8,7 @@ import sys
 
 from conftest import ROOT
 
-GPU_TESTS = {"test_gpu_acceptance.py": 15, "test_gpu_attention_numerics.py": 198, "test_gpu_bench.py": 4, "test_gpu_decode.py": 29,
+GPU_TESTS = {"test_gpu_acceptance.py": 15, "test_gpu_attention_numerics.py": 231, "test_gpu_bench.py": 4, "test_gpu_decode.py": 29,
              "test_gpu_edges.py": 100, "test_gpu_paged_attention.py": 221, "test_gpu_parity.py": 71, "test_gpu_prefill.py": 14,
              "test_gpu_ragged.py": 17, "test_gpu_round.py": 183, "test_zz_no_alloc.py": 2}
 
