@@ -271,9 +271,9 @@ __device__ inline void leave_nothing(const AttnArgs &a, const AttnPlan &plan, in
 // ids a tile earlier) and written to the other half before the barrier.
 //
 // Bound by the products and the softmax beside them where there are many rows: a prompt of 4096 (32 / 8 heads of
-// 128, bfloat16) takes 156 us, 881 TFLOP/s; the matrix pipes are busy 38% of the time and the vector units, two thirds
+// 128, bfloat16) takes 155 us, 887 TFLOP/s; the matrix pipes are busy 38% of the time and the vector units, two thirds
 // of it exponentials, about half, two waves a SIMD covering for each other.  Bound by bytes where there are few: trees
-// of 4 x 16 nodes behind 8192 tokens 33.8 us, 4.0 TB/s.  256 rows a workgroup instead of 128 took the prompt from 233
+// of 4 x 16 nodes behind 8192 tokens 34 us, 4.0 TB/s.  256 rows a workgroup instead of 128 took the prompt from 233
 // to 205 us (staging registers and page look-ups shared by twice the rows), operands read four products ahead 205 to 195.
 template <typename T, int D, int BM>
 __global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 1 : 2) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
@@ -635,8 +635,8 @@ __global__ __launch_bounds__(64 * group_waves(BM), sizeof(T) == 4 && BM == 64 ? 
 // query rows: each computes the scores of one half of a tile's 64 cache rows against the whole width, the pair
 // exchanges its rows' maxima and the weights (8 KiB a tile through LDS), and each multiplies all of the weights with
 // its half of the columns of V.  Per product a wave reads half as much LDS as with 16 rows, and holds 64 registers
-// of outputs.  Chunks of 2 x 2048 tokens behind 16k (16 / 2 heads, bfloat16) take 1292 us, 706 TFLOP/s (a wave with 16 rows:
-// 1544 us); the matrix pipes are busy 36% of the time, and the two barriers keep the eight waves in step, so that
+// of outputs.  Chunks of 2 x 2048 tokens behind 16k (16 / 2 heads, bfloat16) take 1269 us, 719 TFLOP/s (a wave with 16 rows:
+// 1544 us); the matrix pipes are busy 37% of the time, and the two barriers keep the eight waves in step, so that
 // products and softmax overlap little.  Two barriers a tile: behind the maxima, where K has been read and V of the tile is written, and behind
 // the weights, where K of the next tile is.
 constexpr int kPairRows = 128, kPairThreads = 512;
@@ -969,8 +969,8 @@ __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, 
 // that only this wave uses.  A tile is 8 KiB of K and of V, 64 registers; the next tile's loads are issued as soon
 // as K has gone into the products and V into LDS, and are in flight during the softmax and the second product.
 //
-// 64 lanes of decode behind 16k..32k tokens (32 / 4 heads of 128, float16): 578 us, 5.6 TB/s (a read of as many bytes
-// 510 us); one lane behind 1003 tokens: 6.8 us, and 3.2 us for the join.
+// 64 lanes of decode behind 16k..32k tokens (32 / 4 heads of 128, float16): 580 us, 5.6 TB/s (a read of as many bytes
+// 510 us); one lane behind 1003 tokens: 7 us, and 3.2 us for the join.
 constexpr int kFewWaves = 4, kFewRows = 16;
 constexpr int few_tile(int row_bytes) { return 8192 / row_bytes; }
 
@@ -1334,6 +1334,10 @@ hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
 
 }  // namespace
 
+// By the shape alone: the lanes' lengths are on the device, so `held` below is what the page table has room for.  The
+// figures are of tables as long as the cache.  Under a wider one more parts are cut than the lengths would give, some
+// without a row (one lane of 1003 tokens, 16 / 2 heads of 128: 8 parts, 64 under a table for 128k rows, the join 3.2 us and
+// 6.2; trees of 4 x 16 behind 1000: 15.5 us and 17.2), and the bound of 2048 rows on further rounds is one on capacity.
 AttnPlan attn_plan(const AttnDims &d) {
     AttnPlan p;
     const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
