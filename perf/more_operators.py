@@ -194,7 +194,7 @@ def _random_cache(gen, layers, n_pages, Hkv, page, D):
     step = max(1, (1 << 26) // (Hkv * page * D))
     for at in range(0, layers * n_pages, step):
         x = torch.randn((len(codes[at:at + step]), Hkv, page, D), generator=gen, device="cuda")
-        codes[at:at + step], scales[at:at + step] = _quantised(x, 126)
+        codes[at:at + step], scales[at:at + step] = _quantised(x, 125)
     return codes.view(layers, n_pages, Hkv, page, D // 2), scales.view(layers, n_pages, Hkv, page, D // BLOCK)
 
 
@@ -428,7 +428,7 @@ def _rope(s):
     q = _rotate(_rms(s["q"], s["q_norm"]), cos, sin, case["rot"], case["interleaved"])
     k = _rotate(_rms(s["kx"], s["k_norm"]), cos, sin, case["rot"], case["interleaved"])
     pages, at = _places(s, length[:, None] + i)
-    most = 13 if dt == torch.float16 else 126
+    most = 13 if dt == torch.float16 else 125
     s["k"][0][pages, :, at], s["ks"][0][pages, :, at] = _quantised(k, most)
     s["v"][0][pages, :, at], s["vs"][0][pages, :, at] = _quantised(s["vx"], most)
     return {"q": q.to(dt), **_read(s)}
@@ -605,7 +605,7 @@ def _exact_rope(case, s):
         y[..., at[0]], y[..., at[1]] = z.real, z.imag
         return y
 
-    most = 13 if case["dtype"] == "f16" else 126
+    most = 13 if case["dtype"] == "f16" else 125
     return {"q": one(s["q"], s["q_norm"]), "k": _nearest(one(s["kx"], s["k_norm"]), most)[None],
             "v": _nearest(s["vx"].double(), most)[None]}
 
