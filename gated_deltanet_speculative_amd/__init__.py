@@ -31,6 +31,14 @@ paged key/value cache and the acceptance of the draft:
     draft_accept     -> accept_node, n_accept, next_token (what the commits take)
     kv_commit_layers -> new_len; the accepted paths' cache rows moved together, every layer
 
+and the same over a cache held in 4 bits (include/gdn_kv4.h):
+
+    rope_kv4_write   -> q_out; k and v written as 4-bit numbers with a power of two for every 32
+    paged_attention_kv4 -> out
+    kv4_commit_layers -> new_len
+    kv4_read_layers  -> rows of every layer's cache as values
+    kv4_cache        -> a cache of zeros
+
 The library is loaded on first use and must have been built
 (`python -m gated_deltanet_speculative_amd.build`); there is no fallback path.
 """
@@ -77,4 +85,14 @@ from ._round import (  # noqa: F401
     paged_attention,
     paged_attention_workspace_size,
     rope_kv_write,
+)
+from ._kv4 import (  # noqa: F401
+    KV4_EXPORTED,
+    Kv4Cache,
+    kv4_cache,
+    kv4_commit_layers,
+    kv4_read_layers,
+    paged_attention_kv4,
+    paged_attention_kv4_workspace_size,
+    rope_kv4_write,
 )

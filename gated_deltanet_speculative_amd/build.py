@@ -25,7 +25,7 @@ ARCH = "gfx950"
 
 SOURCES = ["gdn_api.cpp", "conv_tree_step.hip", "tree_verify.hip", "replay_commit.hip", "decode_step.hip",
            "prefill.hip", "round_api.cpp", "rope_kv_write.hip", "paged_attention.hip", "draft_accept.hip",
-           "kv_commit.hip"]
+           "kv_commit.hip", "kv4_api.cpp", "paged_attention_kv4.hip", "kv4_read.hip"]
 
 # Packed-FP32 instructions are disabled: the compiler may otherwise fuse ordinary
 # float code into them.
@@ -92,7 +92,7 @@ def build(verbose: bool = True, binding: bool = True) -> str:
     """Builds the library and, with `binding`, the tensor checks; the library is there before a failure of the
     latter is raised."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
         marshal = ex.submit(_build_marshal) if binding else None
         _link(list(ex.map(_compile, SOURCES)))
     if verbose:

@@ -1,0 +1,102 @@
+// Rows of 4-bit caches as values, for gfx950: every layer's rows first .. first + N_c - 1 of the lanes' slots.
+//
+// Bound by bytes: 0.53 of a value read and 2 or 4 bytes of it written.  A lane carries 8 values (a word of codes): D / 8
+// lanes a row, consecutive (row, head) pairs of one layer, K and V in consecutive lanes' order of the output, so
+// that stores are whole lines.  A workgroup finds its tokens' pages first, one thread a token.
+#include "round_device.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 16;  // tokens of a workgroup
+
+template <typename T>
+__device__ inline void four_out(T *p, int w, unsigned scale) {
+    const float s = __uint_as_float(scale << 23);
+    if constexpr (sizeof(T) == 4) {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+        const f2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+        *reinterpret_cast<v4f *>(p) = v4f{a[0], a[1], b[0], b[1]};
+        *reinterpret_cast<v4f *>(p + 4) = v4f{c[0], c[1], d[0], d[1]};
+    } else if constexpr (__is_same(T, __bf16)) {
+        *reinterpret_cast<v4i *>(p) = v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+    } else {
+        *reinterpret_cast<v4i *>(p) = v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
+    }
+}
+
+// Grid: (tokens / kTokens, lanes, layers), K and V one after the other.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(AttnDims d, Cache4Layers cl, PagedLanes l,
+                                                            const int32_t *__restrict__ first_row, T *__restrict__ k_out,
+                                                            T *__restrict__ v_out) {
+    __shared__ int s_row[kTokens];  // cache row of a token for kv head 0, -1 without a page
+    const int tid = threadIdx.x, c = blockIdx.y, layer = blockIdx.z, i0 = blockIdx.x * kTokens;
+    const int slot = l.slot_ids[c], nodes = l.lane_nodes ? l.lane_nodes[c] : d.N, first = first_row[c];
+    if (slot == -1) return;
+    int bits = 0;
+    if (nodes < 0 || nodes > d.N) bits |= GDN_STATUS_NODES;
+    if (slot < -1 || slot >= d.P) bits |= GDN_STATUS_SLOT_RANGE;
+    if (first < 0 || (int64_t)first + max(nodes, 0) > (int64_t)d.max_pages * d.page.d) bits |= GDN_STATUS_LENGTH;
+    if (bits) {
+        if (tid == 0 && i0 == 0 && layer == 0 && l.status) atomicOr(l.status, bits);
+        return;
+    }
+    const int n = min(nodes - i0, kTokens);
+    if (n <= 0) return;
+    if (tid < n) {
+        const uint32_t t = (uint32_t)(first + i0 + tid), entry = d.page(t);
+        const int pid = l.page_table[(int64_t)slot * d.max_pages + entry];
+        const bool paged = (unsigned)pid < (unsigned)d.n_pages;
+        s_row[tid] = paged ? (int)cache_row(d, pid, 0, t, entry) : -1;
+        if (!paged && layer == 0 && l.status) atomicOr(l.status, GDN_STATUS_PAGE);
+    }
+    lds_barrier();
+    constexpr int LPR = D / 8;  // lanes a row
+    const size_t out0 = (((size_t)layer * d.C + c) * d.N + i0) * d.Hkv;
+    for (int side = 0; side < 2; ++side) {
+        T *out = side ? v_out : k_out;
+        if (!out) continue;
+        const int *codes = static_cast<const int *>(side ? cl.codes.v[layer] : cl.codes.k[layer]);
+        const unsigned char *scales = static_cast<const unsigned char *>(side ? cl.scales.v[layer] : cl.scales.k[layer]);
+        for (int k = tid; k < n * d.Hkv * LPR; k += kThreads) {
+            const int sub = k % LPR, r = k / LPR, i = r / d.Hkv, h = r - i * d.Hkv;
+            if (s_row[i] < 0) continue;
+            const size_t row = (size_t)s_row[i] + (size_t)h * d.page.d;
+            four_out<T>(out + (out0 + r) * D + 8 * sub, codes[row * LPR + sub], scales[row * (D / 32) + sub / 4]);
+        }
+    }
+}
+
+template <typename T>
+hipError_t launch(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l, const int32_t *first_row,
+                  void *k_out, void *v_out, hipStream_t stream) {
+    const dim3 grid((d.N + kTokens - 1) / kTokens, d.C, n_layers);
+    T *k = static_cast<T *>(k_out), *v = static_cast<T *>(v_out);
+    if (d.D == 64)
+        hipLaunchKernelGGL((kv4_read_kernel<T, 64>), grid, dim3(kThreads), 0, stream, d, cl, l, first_row, k, v);
+    else if (d.D == 128)
+        hipLaunchKernelGGL((kv4_read_kernel<T, 128>), grid, dim3(kThreads), 0, stream, d, cl, l, first_row, k, v);
+    else
+        hipLaunchKernelGGL((kv4_read_kernel<T, 256>), grid, dim3(kThreads), 0, stream, d, cl, l, first_row, k, v);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv4_read(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l,
+                           const int32_t *first_row, void *k_out, void *v_out, hipStream_t stream) {
+    if (d.dtype == GDN_DTYPE_BF16) return launch<__bf16>(d, n_layers, cl, l, first_row, k_out, v_out, stream);
+    if (d.dtype == GDN_DTYPE_F16) return launch<_Float16>(d, n_layers, cl, l, first_row, k_out, v_out, stream);
+    return launch<float>(d, n_layers, cl, l, first_row, k_out, v_out, stream);
+}
+
+}  // namespace gdn

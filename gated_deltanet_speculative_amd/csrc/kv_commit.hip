@@ -5,7 +5,8 @@
 // a_j >= j, and a row that is written (L + j) is read only by the steps i <= j (a_i >= i): in
 // ascending order, loads of a step before the stores of the same and later ones, the move is safe
 // in place.  A thread owns a 16-byte column of every row of one (lane, layer, K or V) and kv head:
-// no other thread reads or writes it, so the order within the thread is enough.
+// no other thread reads or writes it, so the order within the thread is enough.  Of a 4-bit cache's rows, the codes are such
+// columns and a row's scales (2 to 8 bytes) one column more.
 //
 // Bound by launch and by dependent reads (slot, length, page id, row): every workgroup checks all lanes itself, as
 // in the replay commit, so one launch decides; its own rows are found and the first of them loaded ahead of the
@@ -21,9 +22,36 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 8;  // preflight entries of a thread that are requested together
 constexpr int kAhead = 8;  // moved rows of a thread in flight
 
-__global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers, CacheLayers cl, PagedLanes l,
-                                                             const int32_t *__restrict__ accept_node,
-                                                             int32_t *__restrict__ new_len, int row_chunks) {
+// B bytes (a power of two, at most 16) at an address that is a multiple of B
+template <int B>
+__device__ inline v4i load_bytes(const char *p) {
+    v4i v{};
+    if constexpr (B == 2) v[0] = *reinterpret_cast<const unsigned short *>(p);
+    if constexpr (B == 4) v[0] = *reinterpret_cast<const int *>(p);
+    if constexpr (B == 8) {
+        typedef int v2 __attribute__((ext_vector_type(2)));
+        const v2 x = *reinterpret_cast<const v2 *>(p);
+        v[0] = x[0], v[1] = x[1];
+    }
+    if constexpr (B == 16) v = *reinterpret_cast<const v4i *>(p);
+    return v;
+}
+template <int B>
+__device__ inline void store_bytes(char *p, v4i v) {
+    if constexpr (B == 2) *reinterpret_cast<unsigned short *>(p) = (unsigned short)v[0];
+    if constexpr (B == 4) *reinterpret_cast<int *>(p) = v[0];
+    if constexpr (B == 8) {
+        typedef int v2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<v2 *>(p) = v2{v[0], v[1]};
+    }
+    if constexpr (B == 16) *reinterpret_cast<v4i *>(p) = v;
+}
+
+// kScales: bytes of a row's scales in a 4-bit cache (cl its codes, sc its scales), 0 without them (sc is cl)
+template <int kScales>
+__device__ __forceinline__ void kv_commit(const AttnDims &d, int n_layers, const CacheLayers &cl, const CacheLayers &sc,
+                                          const PagedLanes &l, const int32_t *__restrict__ accept_node,
+                                          int32_t *__restrict__ new_len, int row_chunks) {
     __shared__ unsigned s_bitmap[kBitmapSlots / 32];
     __shared__ int s_word, s_bits;
     __shared__ int s_slot[GDN_MAX_SEQS], s_len[GDN_MAX_SEQS], s_nodes[GDN_MAX_SEQS];  // slot -1: padding or in error
@@ -57,17 +85,30 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
     }
     if (tid == 0) s_bits = 0;
     lds_barrier();
-    // this thread's column: K or V of a layer, kv head, 16 bytes
-    const int cols = d.Hkv * row_chunks, item = blockIdx.x * kThreads + tid, side = item / cols, col = item - side * cols;
+    // this thread's column: K or V of a layer, kv head, 16 bytes; behind the last one of these the scales' columns
+    const int cols = d.Hkv * row_chunks, all = 2 * n_layers * cols, item = blockIdx.x * kThreads + tid;
+    const bool scales = kScales && item >= all;
+    const int per = scales ? d.Hkv : cols, at = scales ? item - all : item, side = at / per, col = at - side * per;
     const bool mine = !lengths && side < 2 * n_layers;
-    v4i *p = nullptr, v[kAhead];
-    if (mine)
-        p = static_cast<v4i *>(side < n_layers ? cl.k[side] : cl.v[side - n_layers]) +
-            (size_t)(col / row_chunks) * d.page.d * row_chunks + col % row_chunks;
+    const int chunks = scales ? 1 : row_chunks;
+    const size_t row_bytes = scales ? kScales : 16 * (size_t)row_chunks;
+    char *p = nullptr;
+    v4i v[kAhead];
+    if (mine) {
+        const CacheLayers &of = scales ? sc : cl;
+        p = static_cast<char *>(side < n_layers ? of.k[side] : of.v[side - n_layers]) +
+            (size_t)(col / chunks) * d.page.d * row_bytes + 16 * (col % chunks);
+    }
     auto load = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (j0 + j < n) v[j] = p[(size_t)s_src[j0 + j] * row_chunks];
+            if (j0 + j < n) {
+                const char *from = p + s_src[j0 + j] * row_bytes;
+                if (scales)
+                    v[j] = load_bytes<kScales>(from);
+                else
+                    v[j] = load_bytes<16>(from);
+            }
     };
     if (mine) load(first);
 
@@ -135,8 +176,26 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_l
         if (j0 != first) load(j0);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (j0 + j < n) p[(size_t)s_dst[j0 + j] * row_chunks] = v[j];
+            if (j0 + j < n) {
+                char *to = p + s_dst[j0 + j] * row_bytes;
+                if (scales)
+                    store_bytes<kScales>(to, v[j]);
+                else
+                    store_bytes<16>(to, v[j]);
+            }
     }
+}
+
+__global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers, CacheLayers cl, PagedLanes l,
+                                                             const int32_t *__restrict__ accept_node,
+                                                             int32_t *__restrict__ new_len, int row_chunks) {
+    kv_commit<0>(d, n_layers, cl, cl, l, accept_node, new_len, row_chunks);
+}
+template <int kScales>
+__global__ __launch_bounds__(kThreads) void kv4_commit_kernel(AttnDims d, int n_layers, Cache4Layers cl, PagedLanes l,
+                                                              const int32_t *__restrict__ accept_node,
+                                                              int32_t *__restrict__ new_len, int row_chunks) {
+    kv_commit<kScales>(d, n_layers, cl.codes, cl.scales, l, accept_node, new_len, row_chunks);
 }
 
 }  // namespace
@@ -150,6 +209,21 @@ hipError_t launch_kv_commit(const AttnDims &d, int n_layers, const CacheLayers &
     const int64_t items = 2ll * layers * d.Hkv * row_chunks;  // columns of a lane, one a thread
     hipLaunchKernelGGL(kv_commit_kernel, dim3((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1),
                        dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_commit(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l,
+                             const int32_t *accept_node, int32_t *new_len, hipStream_t stream) {
+    const int layers = l.parents ? n_layers : 0;
+    const int row_chunks = d.D / 32;  // D / 2 bytes of codes
+    const int64_t items = 2ll * layers * d.Hkv * (row_chunks + 1);
+    const dim3 grid((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1);
+    if (d.D == 64)
+        hipLaunchKernelGGL((kv4_commit_kernel<2>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+    else if (d.D == 128)
+        hipLaunchKernelGGL((kv4_commit_kernel<4>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+    else
+        hipLaunchKernelGGL((kv4_commit_kernel<8>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     return hipGetLastError();
 }
 

@@ -1,0 +1,85 @@
+// Attention over the paged cache of 4-bit values, for gfx950: the kernels of paged_attention.h with rows that become
+// values of the queries' type on their way into LDS (many query rows) or into an operand (few), how a call is divided
+// over them, and their launches.
+#include "paged_attention.h"
+
+namespace gdn {
+namespace {
+
+template <typename T, int D, int BM>
+__global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) void attn_rows_kv4_kernel(AttnArgs a, AttnPlan plan) {
+    attn_rows<T, D, BM, true>(a, plan);
+}
+template <typename T>
+__global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kv4_kernel(AttnArgs a, AttnPlan plan) {
+    attn_pair<T, true>(a, plan);
+}
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kv4_kernel(AttnArgs a, AttnPlan plan) {
+    attn_few<T, D, true>(a, plan);
+}
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kv4_kernel(AttnArgs a, AttnPlan plan) {
+    attn_join<T, D>(a, plan);
+}
+
+template <typename T, int D, int BM>
+void launch_rows(const AttnArgs &a, const AttnPlan &p, unsigned units, hipStream_t stream) {
+    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
+    hipLaunchKernelGGL((attn_rows_kv4_kernel<T, D, BM>), grid, dim3(64 * group_waves(BM)), 0, stream, a, p);
+}
+
+template <typename T, int D>
+hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    constexpr int RB = D * sizeof(T);
+    const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
+    if (p.rows_per_group == kFewRows)
+        hipLaunchKernelGGL((attn_few_kv4_kernel<T, D>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
+    if constexpr (RB < 512 || sizeof(T) == 4)
+        if (p.rows_per_group == 64) launch_rows<T, D, 64>(a, p, units, stream);
+    if constexpr (RB < 512 && sizeof(T) == 2)
+        if (p.rows_per_group == 256) launch_rows<T, D, 256>(a, p, units, stream);
+    if constexpr (D == 256 && sizeof(T) == 2) {
+        if (p.rows_per_group == kPairRows)
+            hipLaunchKernelGGL((attn_pair_kv4_kernel<T>), dim3(p.tiles > 1 ? (units + 7) / 8 * 8 : units), dim3(kPairThreads), 0,
+                               stream, a, p);
+    } else if constexpr (RB < 1024) {
+        if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
+    }
+    if (p.splits > 1) {
+        const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
+        hipLaunchKernelGGL((attn_join_kv4_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
+                           dim3(64 * kJoinWaves), 0, stream, a, p);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    if (a.d.D == 64) return launch<T, 64>(a, p, stream);
+    if (a.d.D == 128) return launch<T, 128>(a, p, stream);
+    return launch<T, 256>(a, p, stream);
+}
+
+}  // namespace
+
+// As attn_plan; few query rows take the kernel for few in every type, as its tiles of K are codes.
+AttnPlan attn_plan_kv4(const AttnDims &d) {
+    const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
+    const int64_t rows = (int64_t)d.N * d.G;
+    if (rows > kFewRows) return attn_plan(d);
+    AttnPlan p{kFewRows, 1, 1};
+    const int64_t groups = (int64_t)d.C * d.Hkv, least = few_tile(row_bytes, true) * kFewWaves, held = (int64_t)d.max_pages * d.page.d;
+    const int64_t most = std::min<int64_t>((held + least - 1) / least, 64), round = 512;
+    p.splits = (int)std::min<int64_t>(most, groups < round ? round / groups : 1);
+    return p;
+}
+
+hipError_t launch_paged_attention_kv4(const AttnArgs &a, hipStream_t stream) {
+    const AttnPlan p = attn_plan_kv4(a.d);
+    if (a.d.dtype == GDN_DTYPE_BF16) return launch_t<__bf16>(a, p, stream);
+    if (a.d.dtype == GDN_DTYPE_F16) return launch_t<_Float16>(a, p, stream);
+    return launch_t<float>(a, p, stream);
+}
+
+}  // namespace gdn

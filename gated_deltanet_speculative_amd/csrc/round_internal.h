@@ -51,13 +51,15 @@ struct RopeArgs {
     const float *q_norm, *k_norm;
     float eps;
     void *k_cache, *v_cache, *q_out;
+    void *k_scales, *v_scales;  // of a 4-bit cache (the two above are its codes), else null
 };
 hipError_t launch_rope_kv_write(const RopeArgs &a, hipStream_t stream);
 
 struct AttnArgs {
     AttnDims d;
     PagedLanes l;
-    const void *q, *k_cache, *v_cache;
+    const void *q, *k_cache, *v_cache;  // a 4-bit cache's codes
+    const void *k_scales, *v_scales;    // and its scales, else null
     float scale_log2;  // scale * log2(e)
     HeadsView gate;    // p null: no gate
     int gate_mode;
@@ -71,17 +73,28 @@ struct AttnPlan {
     int splits;          // parts of the cache, joined by a second launch if more than one
 };
 AttnPlan attn_plan(const AttnDims &d);
-inline size_t attn_workspace_floats(const AttnDims &d) {
-    const AttnPlan p = attn_plan(d);
+AttnPlan attn_plan_kv4(const AttnDims &d);
+inline size_t attn_workspace_floats(const AttnDims &d, const AttnPlan &p) {
     return p.splits == 1 ? 0 : (size_t)p.splits * d.C * d.N * d.Hq * (d.D + 2);
 }
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t stream);
+hipError_t launch_paged_attention_kv4(const AttnArgs &a, hipStream_t stream);
 
 struct CacheLayers {
     void *k[GDN_MAX_LAYERS], *v[GDN_MAX_LAYERS];
 };
 hipError_t launch_kv_commit(const AttnDims &d, int n_layers, const CacheLayers &cl, const PagedLanes &l,
                             const int32_t *accept_node, int32_t *new_len, hipStream_t stream);
+
+// 4-bit caches of a call's layers: codes in `codes`, scales in `scales`
+struct Cache4Layers {
+    CacheLayers codes, scales;
+};
+hipError_t launch_kv4_commit(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l,
+                             const int32_t *accept_node, int32_t *new_len, hipStream_t stream);
+// Rows from first_row on as values; either output may be null
+hipError_t launch_kv4_read(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l,
+                           const int32_t *first_row, void *k_out, void *v_out, hipStream_t stream);
 
 struct AcceptArgs {
     int C, N, V, dtype;
