@@ -39,6 +39,11 @@ and the same over a cache held in 4 bits (include/gdn_kv4.h):
     kv4_read_layers  -> rows of every layer's cache as values
     kv4_cache        -> a cache of zeros
 
+and between the target's logits and the acceptance (include/gdn_logits.h):
+
+    adjust_logits    -> penalties for repeated tokens, biases, grammar masks; with temperatures, the
+                        probabilities that draft_accept takes
+
 The library is loaded on first use and must have been built
 (`python -m gated_deltanet_speculative_amd.build`); there is no fallback path.
 """
@@ -95,4 +100,11 @@ from ._kv4 import (  # noqa: F401
     paged_attention_kv4,
     paged_attention_kv4_workspace_size,
     rope_kv4_write,
+)
+from ._logits import (  # noqa: F401
+    LOGITS_EXPORTED,
+    LogitsShape,
+    STATUS_RULE,
+    adjust_logits,
+    adjust_logits_workspace_size,
 )

@@ -25,7 +25,8 @@ ARCH = "gfx950"
 
 SOURCES = ["gdn_api.cpp", "conv_tree_step.hip", "tree_verify.hip", "replay_commit.hip", "decode_step.hip",
            "prefill.hip", "round_api.cpp", "rope_kv_write.hip", "paged_attention.hip", "draft_accept.hip",
-           "kv_commit.hip", "kv4_api.cpp", "paged_attention_kv4.hip", "kv4_read.hip"]
+           "kv_commit.hip", "kv4_api.cpp", "paged_attention_kv4.hip", "kv4_read.hip",
+           "logits_api.cpp", "adjust_logits.hip"]
 
 # Packed-FP32 instructions are disabled: the compiler may otherwise fuse ordinary
 # float code into them.
