@@ -36,11 +36,35 @@ __device__ inline Best wave_best(Best b) {
     for (int k = 1; k < 64; k <<= 1) b = better(b, Best{__shfl_xor(b.v, k), __shfl_xor(b.x, k)});
     return b;
 }
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) x += __shfl_xor(x, k);
-    return x;
+// Largest and sum over a wave, the same in every lane: rotations within the rows of 16 lanes (no LDS), then the four rows
+template <int N>
+__device__ inline float row_rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xF, 0xF, false));
 }
+__device__ inline float lane_of(float x, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), j)); }
+// (as integers of the same order, whose maximum takes no quieting of NaN; a NaN is above infinity there)
+__device__ inline int ordered(float x) { return __float_as_int(x) ^ ((__float_as_int(x) >> 31) & 0x7fffffff); }
+template <int N>
+__device__ inline int row_rotated(int x) { return __builtin_amdgcn_update_dpp(x, x, 0x120 + N, 0xF, 0xF, false); }
+__device__ inline float wave_max(float v) {
+    int x = ordered(v);
+    x = max(x, row_rotated<8>(x));
+    x = max(x, row_rotated<4>(x));
+    x = max(x, row_rotated<2>(x));
+    x = max(x, row_rotated<1>(x));
+    const int a = max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16));
+    const int b = max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48));
+    const int top = max(a, b);
+    return __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+}
+__device__ inline float wave_sum(float x) {
+    x += row_rotated<8>(x);
+    x += row_rotated<4>(x);
+    x += row_rotated<2>(x);
+    x += row_rotated<1>(x);
+    return (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
+}
+constexpr int kAhead = 4;  // loads of a thread that are requested together
 // log2(e) / T within the normal numbers: finite for T = 0, and never 0, so that -infinity times it is -infinity
 __device__ inline float per_temperature(float temp) { return fminf(fmaxf(1.4426950408889634f / temp, 0x1p-126f), 3.4e38f); }
 // e^{(z - m) / T} with k = log2(e) / T; 1 at the maximum even where that is infinite, 0 for -infinity
@@ -49,24 +73,138 @@ __device__ inline float weight(float z, float m, float k) {
     return __builtin_amdgcn_exp2f(z == top ? 0.f : (z - top) * k);
 }
 
-template <typename T, typename O, int W, int MODE>
-__global__ __launch_bounds__(kThreads) void adjust_logits_kernel(LogitArgs a) {
-    constexpr int VEC = 16 / sizeof(T), GR = W / VEC, kChunk = kThreads * W;
+// Entries of a slot's history from k0 on, four at a time: entry 4 (j kThreads + tid) + k0 and the next three, or, where
+// these would pass the end, the last four (of which `from` leaves out what another thread has; fewer than four in all:
+// one at a time).
+struct Past {
+    typedef int v4a __attribute__((ext_vector_type(4), aligned(4)));
+    v4a t[kAhead];
+    __device__ static int from(int k0, int j) { return k0 + 4 * (j * kThreads + (int)threadIdx.x); }
+    __device__ static int at(const LogitArgs &a, int k0, int j) { return max(min(from(k0, j), a.H - 4), 0); }
+    __device__ void load(const LogitArgs &a, int slot, int k0) {
+        const int32_t *p = a.r.history + (int64_t)slot * a.H;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            t[j] = v4a{-1, -1, -1, -1};
+            if (k0 + 4 * j * kThreads >= a.H) continue;  // (the same for every thread)
+            if (a.H >= 4) {
+                t[j] = *reinterpret_cast<const v4a *>(p + at(a, k0, j));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < a.H) t[j][e] = p[e];
+            }
+        }
+    }
+};
+
+// A row's maximum, sum of exponentials below it and place of the maximum.  Every wave that has a piece of the row leaves
+// its own; by a wave, the whole from these: a lane takes every 64th, in order, the lanes are joined in a fixed tree.
+struct Total {
+    float top, sum;
+    int at;
+};
+constexpr int kParts = 4;  // a lane's parts that are requested together
+struct Parts {
+    v4f v[kParts];
+    __device__ static const v4f *of(const LogitArgs &a, int c, int i) {
+        return reinterpret_cast<const v4f *>(a.stats) + ((size_t)c * a.N + i) * gridDim.x * kWaves;
+    }
+    __device__ void load(const v4f *row, int k0) {
+        const int parts = gridDim.x * kWaves;
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+            const int k = k0 + 64 * j + (int)(threadIdx.x & 63);
+            v[j] = row[min(k, parts - 1)];
+            if (k >= parts) v[j] = v4f{kNegInf, 0.f, __int_as_float(0x7fffffff), 0.f};
+        }
+    }
+};
+__device__ inline Total row_total(const LogitArgs &a, int c, int i, float temp, Parts &p) {  // p: the first ones, loaded
+    const int parts = gridDim.x * kWaves;
+    const float k2 = per_temperature(temp);
+    const v4f *row = Parts::of(a, c, i);
+    Best b{kNegInf, 0x7fffffff};
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += 64 * kParts) {
+        if (k0) p.load(row, k0);
+        Best to = b;
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) to = better(to, Best{p.v[j][0], __float_as_int(p.v[j][2])});
+        if (k0) sum = sum == 0.f ? 0.f : sum * weight(b.v, to.v, k2);  // (a part of nothing has sum 0; NaN sums stay NaN)
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) sum += p.v[j][1] == 0.f ? 0.f : p.v[j][1] * weight(p.v[j][0], to.v, k2);
+        b = to;
+    }
+    Best all{wave_max(b.v), 0x7fffffff};
+    if (temp == 0.f) all = wave_best(b);
+    return Total{all.v, wave_sum(sum == 0.f ? 0.f : sum * weight(b.v, all.v, k2)), all.x};
+}
+
+template <typename T, typename O, int MODE>
+__global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a) {
+    constexpr int W = kLogitTokens, VEC = 16 / sizeof(T), GR = W / VEC, kChunk = kLogitChunk;
     typedef T tv __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
     typedef O ov __attribute__((ext_vector_type(VEC), aligned(sizeof(O))));
-    typedef int v4a __attribute__((ext_vector_type(4), aligned(4)));
     __shared__ __attribute__((aligned(16))) unsigned s_word[kChunk];
     __shared__ __attribute__((aligned(16))) float s_bias[kChunk];
-    __shared__ int s_tok[GDN_MAX_NODES], s_again;
+    __shared__ int s_again;
     __shared__ unsigned s_anc[GDN_MAX_NODES];
-    __shared__ float s_max[GDN_MAX_NODES], s_inv[GDN_MAX_NODES];
-    __shared__ int s_best[GDN_MAX_NODES];
+    __shared__ Total s_total[GDN_MAX_NODES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = blockIdx.y, x0 = blockIdx.x * kChunk;
     const int i0 = blockIdx.z * a.rows;
 
-    // ---- the lane's checks; every wave of every workgroup comes to the same verdict
     const int slot = a.slot_ids[c], nodes = a.lane_nodes ? a.lane_nodes[c] : a.N;
     if (slot == -1) return;
+    // ---- requested ahead of the checks: the tree, a row's parts, the first row (every node has one, present or not), the first of the history
+    // (its length not known yet: what lies behind it is not counted) and the biases of the slot
+    const bool in_lane = lane < a.N;  // (at most 32)
+    const int64_t node = (int64_t)c * a.N + min(lane, a.N - 1);
+    int parent = lane - 1, tok = -1;
+    if (a.parents) parent = a.parents[node];
+    if (a.tokens) tok = a.tokens[node];
+    Parts parts;
+    if constexpr (MODE == kProbabilities) parts.load(Parts::of(a, c, min(i0 + wave, a.N - 1)), 0);
+    const int mask_words = (a.V + 31) / 32;
+    tv raw[GR];
+    unsigned allow[GR];
+    auto load = [&](int i) {
+        const int64_t row = (int64_t)c * a.N + i;
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+            const int x = x0 + (g * kThreads + tid) * VEC;
+            if (x + VEC <= a.V) {
+                raw[g] = *reinterpret_cast<const tv *>(p + x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) raw[g][e] = x + e < a.V ? p[x + e] : (T)0.f;
+            }
+            allow[g] = (1u << VEC) - 1u;
+            if (a.mask && x < a.V) allow[g] = (unsigned)a.mask[row * mask_words + x / 32] >> (x & 31);
+            if (x + VEC > a.V) allow[g] &= x < a.V ? (1u << (a.V - x)) - 1u : 0u;
+        }
+    };
+    load(i0);
+    const int known = slot < -1 || slot >= a.P ? 0 : slot;
+    Past past;
+    if (a.r.history) past.load(a, known, 0);
+    constexpr int kBiases = (1024 + kThreads - 1) / kThreads;
+    int bias_tok[kBiases];
+    float bias_val[kBiases];
+    if (a.r.bias_tokens)
+#pragma unroll
+        for (int j = 0; j < kBiases; ++j) {
+            bias_tok[j] = -1;
+            if (j * kThreads < a.B) {  // (the same for every thread)
+                const int64_t at = (int64_t)known * a.B + min(j * kThreads + tid, a.B - 1);
+                bias_tok[j] = a.r.bias_tokens[at];
+                bias_val[j] = a.r.bias[at];
+            }
+        }
+
+    // ---- the lane's checks; every wave of every workgroup comes to the same verdict
     int bits = 0;
     if (nodes < 0 || nodes > a.N) bits |= GDN_STATUS_NODES;
     float rep = 1.f, pres = 0.f, freq = 0.f, temp = 1.f;
@@ -85,15 +223,10 @@ __global__ __launch_bounds__(kThreads) void adjust_logits_kernel(LogitArgs a) {
             bits |= GDN_STATUS_RULE;
         if (held < 0 || held > a.H || prompt < 0 || prompt > held) bits |= GDN_STATUS_LENGTH;
     }
-    int tok = -1;
-    unsigned anc = 0;
+    const bool has = in_lane && lane < nodes;
+    if (!has) tok = -1;
     if (!(bits & GDN_STATUS_NODES)) {
-        const bool has = lane < nodes;  // (at most 32)
-        anc = has ? (2u << lane) - 1u : 0u;
-        bool bad = false;
-        if (a.parents) anc = tree_ancestors(a.parents + (int64_t)c * a.N, nodes, bad);
-        if (bad) bits |= GDN_STATUS_PARENT;
-        if (a.tokens && has) tok = a.tokens[(int64_t)c * a.N + lane];
+        if (__builtin_amdgcn_ballot_w64(has && (parent < -1 || parent >= lane))) bits |= GDN_STATUS_PARENT;
         if (__builtin_amdgcn_ballot_w64(a.tokens && has && (unsigned)tok >= (unsigned)a.V)) bits |= GDN_STATUS_TOKEN;
     }
     if (bits) {
@@ -102,203 +235,214 @@ __global__ __launch_bounds__(kThreads) void adjust_logits_kernel(LogitArgs a) {
     }
     const int i1 = min(i0 + a.rows, nodes);
     if (i0 >= i1) return;
+    const unsigned inside = min(kChunk, a.V - x0);  // (an id outside the stretch, or the vocabulary, is not below it from x0 on)
 
     // ---- the stretch's words
-#pragma unroll
-    for (int k = 0; k < W / 4; ++k) reinterpret_cast<v4i *>(s_word)[k * kThreads + tid] = v4i{0, 0, 0, 0};
     const bool biased = a.r.bias_tokens && a.B > 0;
-    if (biased)
 #pragma unroll
-        for (int k = 0; k < W / 4; ++k) reinterpret_cast<v4f *>(s_bias)[k * kThreads + tid] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (tid < GDN_MAX_NODES) {
-        s_tok[tid] = tok;
-        s_anc[tid] = anc;
+    for (int k = 0; k < W / 4; ++k) {
+        reinterpret_cast<v4i *>(s_word)[k * kThreads + tid] = v4i{0, 0, 0, 0};
+        if (biased) reinterpret_cast<v4f *>(s_bias)[k * kThreads + tid] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     if (tid == 0) s_again = 0;
-    if constexpr (MODE == kProbabilities) {  // the rows' maxima and sums, a row a wave
-        const int parts = gridDim.x * kWaves;
-        const float k2 = per_temperature(temp);
-        for (int i = i0 + wave; i < i1; i += kWaves) {
-            const v4f *st = reinterpret_cast<const v4f *>(a.stats) + ((size_t)c * a.N + i) * parts;
-            Best b{kNegInf, 0x7fffffff};
-            for (int k = lane; k < parts; k += 64) b = better(b, Best{st[k][0], __float_as_int(st[k][2])});
-            b = wave_best(b);
-            float sum = 0.f;
-            for (int k = lane; k < parts; k += 64) {
-                const float m = st[k][0], s = st[k][1];
-                if (s != 0.f) sum += s * weight(m, b.v, k2);
+    if (a.tokens && wave == kWaves - 1) {  // (while the history is on its way)
+        bool bad;
+        const unsigned anc = a.parents ? tree_sets(parent, has, bad) : has ? (2u << lane) - 1u : 0u;
+        if (lane < GDN_MAX_NODES) s_anc[lane] = anc;
+    }
+    if constexpr (MODE == kProbabilities)
+        for (int i = i0 + wave; i < i1; i += kWaves) {  // a row a wave
+            if (i != i0 + wave) parts.load(Parts::of(a, c, i), 0);
+            const Total t = row_total(a, c, i, temp, parts);
+            if (lane == 0) s_total[i - i0] = t;
+        }
+    lds_barrier();
+    if (a.r.history) {
+#pragma unroll 1
+        for (int k0 = 0; k0 == 0 || k0 < held; k0 += 4 * kThreads * kAhead) {
+            if (k0) past.load(a, slot, k0);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (k0 + 4 * j * kThreads >= held) continue;  // (the same for every thread)
+                const int at = past.at(a, k0, j), low = past.from(k0, j) - at, high = held - at;
+                if (__builtin_amdgcn_ballot_w64(low > 0 || high < 4))
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) past.t[j][e] = e >= low && e < high ? past.t[j][e] : -1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned x = (unsigned)(past.t[j][e] - x0);
+                    if (x < inside) {
+                        if (at + e >= prompt)
+                            atomicAdd(&s_word[x], 1u);
+                        else
+                            atomicOr(&s_word[x], kPrompt);
+                    }
+                }
             }
-            sum = wave_sum(sum);
-            if (lane == 0) {
-                s_max[i - i0] = b.v;
-                s_inv[i - i0] = sum == 0.f ? 0.f : 1.f / sum;
-                s_best[i - i0] = b.v == kNegInf ? -1 : b.x;
+        }
+    }
+    if ((unsigned)(tok - x0) < inside && tid < GDN_MAX_NODES) atomicOr(&s_word[tok - x0], kDraft);
+    if (biased) {
+#pragma unroll
+        for (int j = 0; j < kBiases; ++j) {
+            const unsigned x = (unsigned)(bias_tok[j] - x0);
+            if (x < inside && j * kThreads + tid < a.B) {
+                if (atomicOr(&s_word[x], kBias) & kBias) s_again = 1;
+                s_bias[x] = bias_val[j];
             }
         }
     }
     lds_barrier();
-    if (held > 0) {
-        const int32_t *past = a.r.history + (int64_t)slot * a.H;
-        auto count = [&](int at, int t) {
-            const int x = t - x0;
-            if ((unsigned)x < (unsigned)kChunk && t < a.V) {
-                if (at >= prompt)
-                    atomicAdd(&s_word[x], 1u);
-                else
-                    atomicOr(&s_word[x], kPrompt);
-            }
-        };
-        const int whole = held / 4;
-        for (int k = tid; k < whole; k += kThreads) {
-            const v4a t = *reinterpret_cast<const v4a *>(past + 4 * k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) count(4 * k + e, t[e]);
-        }
-        if (4 * whole + tid < held && tid < 4) count(4 * whole + tid, past[4 * whole + tid]);
-    }
-    if (tok >= x0 && tok < x0 + kChunk && tid < GDN_MAX_NODES) atomicOr(&s_word[tok - x0], kDraft);
-    if (biased) {
+    if (biased && s_again) {  // a token twice: its first entry's thread adds them up in the list's order
         const int32_t *toks = a.r.bias_tokens + (int64_t)slot * a.B;
         const float *vals = a.r.bias + (int64_t)slot * a.B;
         for (int j = tid; j < a.B; j += kThreads) {
-            const int t = toks[j], x = t - x0;
-            if ((unsigned)x < (unsigned)kChunk && t < a.V) {
-                if (atomicOr(&s_word[x], kBias) & kBias) s_again = 1;
-                s_bias[x] = vals[j];
-            }
+            const int u = toks[j];
+            const unsigned x = (unsigned)(u - x0);
+            if (x >= inside) continue;
+            bool first = true;
+            for (int k = 0; k < j; ++k) first &= toks[k] != u;
+            if (!first) continue;
+            float sum = vals[j];
+            for (int k = j + 1; k < a.B; ++k)
+                if (toks[k] == u) sum += vals[k];
+            s_bias[x] = sum;
         }
         lds_barrier();
-        if (s_again)  // a token twice: its first entry's thread adds them up in the list's order
-            for (int j = tid; j < a.B; j += kThreads) {
-                const int t = toks[j], x = t - x0;
-                if ((unsigned)x >= (unsigned)kChunk || t >= a.V) continue;
-                bool first = true;
-                for (int k = 0; k < j; ++k) first &= toks[k] != t;
-                if (!first) continue;
-                float sum = vals[j];
-                for (int k = j + 1; k < a.B; ++k)
-                    if (toks[k] == t) sum += vals[k];
-                s_bias[x] = sum;
-            }
     }
-    lds_barrier();
-    // ---- this thread's tokens: group g from x0 + (g kThreads + tid) VEC on
-    unsigned w[W];
-    float b[W];
+    // ---- this thread's tokens: group g from x0 + (g kThreads + tid) VEC on.  With r >= 1, v > 0 ? v / r : v r is the smaller
+    // of v / r and v r (with r < 1 the larger), so a logit l becomes the smaller of l up + cu and l down + cd, whose
+    // constants hold the biases and what the occurrences take off.  `on`: the nodes with this token.
+    auto token_of = [&](int q) { return (q / VEC * kThreads + tid) * VEC + q % VEC; };
+    float b[W], up[W], down[W], cu[W], cd[W];
+    unsigned w[W], on[W], drafts = 0;
+    const float inv = 1.f / rep, k2 = per_temperature(temp);
+    const bool shrinks = rep >= 1.f;
 #pragma unroll
-    for (int g = 0; g < GR; ++g)
+    for (int q = 0; q < W; ++q) {
+        w[q] = s_word[token_of(q)];
+        b[q] = biased ? s_bias[token_of(q)] : 0.f;
+        const bool seen = (w[q] & (kCount | kPrompt)) != 0;
+        up[q] = seen ? inv : 1.f;
+        down[q] = seen ? rep : 1.f;
+        const float less = w[q] & kCount ? fmaf(freq, (float)(w[q] & kCount), pres) : 0.f;
+        cu[q] = fmaf(b[q], up[q], -less);
+        cd[q] = fmaf(b[q], down[q], -less);
+        on[q] = 0;
+        drafts |= w[q];
+    }
+    const bool drafted = __builtin_amdgcn_ballot_w64((drafts & kDraft) != 0) != 0;  // (of this wave)
+    if (drafted) {
+        const int base = x0 + __builtin_amdgcn_readfirstlane(tid & ~63) * VEC;  // of the wave's first group
+#pragma unroll 1
+        for (int j = 0; j < nodes; ++j) {
+            const int t = __builtin_amdgcn_readlane(tok, j) - base;
+            if (GR == 1 && (unsigned)t >= 64u * VEC) continue;  // (the same for the wave)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[g * VEC + e] = s_word[(g * kThreads + tid) * VEC + e];
-            b[g * VEC + e] = biased ? s_bias[(g * kThreads + tid) * VEC + e] : 0.f;
+            for (int q = 0; q < W; ++q) on[q] |= t == q / VEC * kThreads * VEC + lane * VEC + q % VEC ? 1u << j : 0u;
         }
-    const float inv = 1.f / rep;
-    const float k2 = per_temperature(temp);
-    const int mask_words = (a.V + 31) / 32;
-
-    tv raw[GR];
-    unsigned allow[GR];
-    auto load = [&](int i) {
-        const int64_t row = (int64_t)c * a.N + i;
-        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-#pragma unroll
-        for (int g = 0; g < GR; ++g) {
-            const int x = x0 + (g * kThreads + tid) * VEC;
-            if (x + VEC <= a.V) {
-                raw[g] = *reinterpret_cast<const tv *>(p + x);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) raw[g][e] = x + e < a.V ? p[x + e] : (T)0.f;
-            }
-            allow[g] = 0xffffffffu;
-            if (a.mask && x < a.V) allow[g] = (unsigned)a.mask[row * mask_words + x / 32] >> (x & 31);
-        }
-    };
-    load(i0);
+    }
+    const bool cut = a.mask || x0 + kChunk > a.V;  // some token of the stretch may not be allowed
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         float z[W];
-        const unsigned path = s_anc[i];
+        if (shrinks) {
 #pragma unroll
-        for (int g = 0; g < GR; ++g)
+            for (int q = 0; q < W; ++q) {
+                const float l = (float)raw[q / VEC][q % VEC];
+                z[q] = fminf(fmaf(l, up[q], cu[q]), fmaf(l, down[q], cd[q]));
+            }
+        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int q = g * VEC + e, x = x0 + (g * kThreads + tid) * VEC + e;
-                unsigned n = w[q] & kCount;
-                bool seen = (w[q] & (kCount | kPrompt)) != 0;
-                if (w[q] & kDraft)
-                    for (unsigned p = path; p; p &= p - 1u)
-                        if (s_tok[__builtin_ctz(p)] == x) ++n, seen = true;
-                float v = (float)raw[g][e] + b[q];
-                const float scaled = v * (v > 0.f ? inv : rep);
-                v = seen ? scaled : v;
-                const float less = fmaf(-freq, (float)n, v) - pres;
-                v = n ? less : v;
-                z[q] = (allow[g] >> e) & 1 && x < a.V ? v : kNegInf;
+            for (int q = 0; q < W; ++q) {
+                const float l = (float)raw[q / VEC][q % VEC];
+                z[q] = fmaxf(fmaf(l, up[q], cu[q]), fmaf(l, down[q], cd[q]));
+            }
+        }
+        if (drafted) {
+            const unsigned path = s_anc[i];
+#pragma unroll
+            for (int q = 0; q < W; ++q) {
+                const unsigned here = on[q] & path, n = (w[q] & kCount) + __popc(here);
+                const float v = (float)raw[q / VEC][q % VEC] + b[q];
+                z[q] = here ? v * (v > 0.f ? inv : rep) - fmaf(freq, (float)n, pres) : z[q];
+            }
+        }
+        if (cut)
+#pragma unroll
+            for (int q = 0; q < W; ++q) {  // (bit by bit: all ones where the token is allowed)
+                const int keep = (int)(allow[q / VEC] << (31 - q % VEC)) >> 31;
+                z[q] = __int_as_float((keep & __float_as_int(z[q])) | (~keep & __float_as_int(kNegInf)));
             }
         if (i + 1 < i1) load(i + 1);
         if constexpr (MODE == kStats) {
             Best top{kNegInf, 0x7fffffff};
+            if (temp > 0.f) {  // (the place of the maximum is for T = 0 only)
 #pragma unroll
-            for (int g = 0; g < GR; ++g)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (z[g * VEC + e] > top.v) top = Best{z[g * VEC + e], x0 + (g * kThreads + tid) * VEC + e};
-            top = wave_best(top);
-            float sum = 0.f;
-#pragma unroll
-            for (int q = 0; q < W; ++q) sum += weight(z[q], top.v, k2);
-            sum = wave_sum(sum);
-            if (lane == 0)
-                reinterpret_cast<v4f *>(a.stats)[((size_t)c * a.N + i) * gridDim.x * kWaves + blockIdx.x * kWaves + wave] =
-                    v4f{top.v, sum, __int_as_float(top.x), 0.f};
-            continue;
-        }
-        if constexpr (MODE == kProbabilities) {
-            const float m = s_max[i - i0], scale = s_inv[i - i0];
-            const int best = s_best[i - i0];
-#pragma unroll
-            for (int g = 0; g < GR; ++g)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int q = g * VEC + e, x = x0 + (g * kThreads + tid) * VEC + e;
-                    z[q] = temp > 0.f ? weight(z[q], m, k2) * scale : x == best ? 1.f : 0.f;
-                }
-        }
-        O *out = static_cast<O *>(a.out) + ((int64_t)c * a.N + i) * a.V;
-#pragma unroll
-        for (int g = 0; g < GR; ++g) {
-            const int x = x0 + (g * kThreads + tid) * VEC;
-            if (x + VEC <= a.V) {
-                ov o;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o[e] = (O)z[g * VEC + e];
-                *reinterpret_cast<ov *>(out + x) = o;
+                for (int q = 0; q < W; ++q) top.v = fmaxf(top.v, z[q]);
+                top.v = wave_max(top.v);
             } else {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (x + e < a.V) out[x + e] = (O)z[g * VEC + e];
+                for (int q = 0; q < W; ++q)
+                    if (z[q] > top.v) top = Best{z[q], x0 + token_of(q)};
+                top = wave_best(top);
+            }
+            float sum = 0.f;
+            if (fabsf(top.v) < __builtin_inff()) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) sum += __builtin_amdgcn_exp2f((z[q] - top.v) * k2);
+            } else {
+#pragma unroll
+                for (int q = 0; q < W; ++q) sum += weight(z[q], top.v, k2);
+            }
+            sum = wave_sum(sum);
+            if (lane == 0)
+                reinterpret_cast<v4f *>(a.stats)[(((size_t)c * a.N + i) * gridDim.x + blockIdx.x) * kWaves + wave] =
+                    v4f{top.v, sum, __int_as_float(top.x), 0.f};
+        } else {
+            if constexpr (MODE == kProbabilities) {
+                const Total t = s_total[i - i0];
+                const float scale = t.sum == 0.f ? 0.f : 1.f / t.sum;
+                if (temp > 0.f && fabsf(t.top) < __builtin_inff()) {
+#pragma unroll
+                    for (int q = 0; q < W; ++q) z[q] = __builtin_amdgcn_exp2f((z[q] - t.top) * k2) * scale;
+                } else {
+                    const int best = t.top == kNegInf ? -1 : t.at;
+#pragma unroll
+                    for (int q = 0; q < W; ++q)
+                        z[q] = temp > 0.f ? weight(z[q], t.top, k2) * scale : x0 + token_of(q) == best ? 1.f : 0.f;
+                }
+            }
+            O *out = static_cast<O *>(a.out) + ((int64_t)c * a.N + i) * a.V;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                const int x = x0 + (g * kThreads + tid) * VEC;
+                if (x + VEC <= a.V) {
+                    ov o;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = (O)z[g * VEC + e];
+                    *reinterpret_cast<ov *>(out + x) = o;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (x + e < a.V) out[x + e] = (O)z[g * VEC + e];
+                }
             }
         }
     }
 }
 
-template <typename T, typename O, int W>
-hipError_t launch_w(const LogitArgs &a, dim3 grid, hipStream_t stream) {
-    if (!a.r.temperature) {
-        hipLaunchKernelGGL((adjust_logits_kernel<T, O, W, kLogits>), grid, dim3(kThreads), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((adjust_logits_kernel<T, O, W, kStats>), grid, dim3(kThreads), 0, stream, a);
-        hipLaunchKernelGGL((adjust_logits_kernel<T, O, W, kProbabilities>), grid, dim3(kThreads), 0, stream, a);
-    }
-    return hipGetLastError();
-}
-
 template <typename T, typename O>
 hipError_t launch(LogitArgs a, hipStream_t stream) {
-    const LogitPlan p = logit_plan(a.C, a.N, a.V);
-    a.rows = p.rows;
-    const dim3 grid(p.chunks(a.V), a.C, (a.N + p.rows - 1) / p.rows);
-    return p.per == 16 ? launch_w<T, O, 16>(a, grid, stream) : launch_w<T, O, 8>(a, grid, stream);
+    a.rows = logit_rows(a.C, a.N, a.V);
+    const dim3 grid(logit_chunks(a.V), a.C, (a.N + a.rows - 1) / a.rows);
+    if (!a.r.temperature) {
+        hipLaunchKernelGGL((adjust_logits_kernel<T, O, kLogits>), grid, dim3(kThreads), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((adjust_logits_kernel<T, O, kStats>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((adjust_logits_kernel<T, O, kProbabilities>), grid, dim3(kThreads), 0, stream, a);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace

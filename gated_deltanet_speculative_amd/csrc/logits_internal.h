@@ -13,26 +13,19 @@ struct LogitArgs {
     gdn_logit_rules r;
     const int32_t *mask, *tokens, *parents, *lane_nodes, *slot_ids;
     void *out;
-    float *stats;  // a row's maximum, sum and place of the maximum, 16 bytes per wave that shares the row
+    float *stats;  // a row's maximum, sum and place of the maximum, 16 bytes per wave that has a piece of it
     int32_t *status;
     int rows;  // nodes of a workgroup
 };
 
-constexpr int kLogitThreads = 256;
-// Tokens of a thread: 16, or 8 where there would be too few workgroups
-struct LogitPlan {
-    int per, rows;  // tokens a thread, nodes a workgroup
-    int chunks(int V) const { return (V + per * kLogitThreads - 1) / (per * kLogitThreads); }
-    int waves(int V) const { return chunks(V) * (kLogitThreads / 64); }
-};
-inline LogitPlan logit_plan(int C, int N, int V) {
-    LogitPlan p{16, N};
-    if ((int64_t)C * N * p.chunks(V) < 1024) p.per = 8;
-    const int64_t groups = (int64_t)C * p.chunks(V), parts = (1023 + groups) / groups;
-    p.rows = parts >= N ? 1 : (int)((N + parts - 1) / parts);
-    return p;
+constexpr int kLogitThreads = 512, kLogitTokens = 8, kLogitChunk = kLogitThreads * kLogitTokens;  // a stretch of the vocabulary
+inline int logit_chunks(int V) { return (V + kLogitChunk - 1) / kLogitChunk; }
+// Nodes of a workgroup: all of a lane's, fewer where there would be less than 512 workgroups
+inline int logit_rows(int C, int N, int V) {
+    const int64_t groups = (int64_t)C * logit_chunks(V), parts = (511 + groups) / groups;
+    return parts >= N ? 1 : (int)((N + parts - 1) / parts);
 }
-inline size_t logit_workspace_bytes(int C, int N, int V) { return (size_t)C * N * logit_plan(C, N, V).waves(V) * 16; }
+inline size_t logit_workspace_bytes(int C, int N, int V) { return (size_t)C * N * logit_chunks(V) * (kLogitThreads / 64) * 16; }
 
 hipError_t launch_adjust_logits(const LogitArgs &a, hipStream_t stream);
 

@@ -31,10 +31,9 @@ __device__ inline Lane paged_lane(const AttnDims &d, const PagedLanes &l, int c)
 // A draft tree of at most GDN_MAX_NODES nodes, one node per lane of a wave: lane i receives the
 // set of i and its ancestors as a bit mask (pointer jumping: five rounds of lane shuffles), and
 // `bad` whether a present node's parent lies outside [-1, i-1].  Every lane of the wave calls it.
-__device__ inline unsigned tree_ancestors(const int32_t *__restrict__ parents, int nodes, bool &bad) {
-    const int lane = threadIdx.x & 63;
-    const bool has = lane < nodes && lane < GDN_MAX_NODES;
-    const int par = has ? parents[lane] : -1;
+// (tree_sets: the same with the lane's parent in a register; has: the lane has a node.)
+__device__ inline unsigned tree_sets(int parent, bool has, bool &bad) {
+    const int lane = threadIdx.x & 63, par = has ? parent : -1;
     bad = __builtin_amdgcn_ballot_w64(has && (par < -1 || par >= lane)) != 0;
     int jump = par >= 0 && par < lane ? par : -1;
     unsigned anc = has ? 1u << lane : 0u;
@@ -49,6 +48,11 @@ __device__ inline unsigned tree_ancestors(const int32_t *__restrict__ parents, i
         }
     }
     return anc;
+}
+__device__ inline unsigned tree_ancestors(const int32_t *__restrict__ parents, int nodes, bool &bad) {
+    const int lane = threadIdx.x & 63;
+    const bool has = lane < nodes && lane < GDN_MAX_NODES;
+    return tree_sets(has ? parents[lane] : -1, has, bad);
 }
 
 // Whether another lane of the call uses slot s (every thread of the workgroup looks at a share

@@ -9,11 +9,11 @@ static int g_launches = 0;
 namespace gdn {
 hipError_t launch_adjust_logits(const LogitArgs &a, hipStream_t) {
     ++g_launches;
-    const LogitPlan p = logit_plan(a.C, a.N, a.V);
-    // every node and token has a workgroup, the grid is within its limits, and the waves' parts fit the workspace
-    const long long groups = (a.N + p.rows - 1) / p.rows;
-    if (p.rows < 1 || p.rows > a.N || groups * p.rows < a.N || (long long)p.chunks(a.V) * p.per * kLogitThreads < a.V ||
-        p.chunks(a.V) > 65535 || logit_workspace_bytes(a.C, a.N, a.V) != (size_t)a.C * a.N * p.chunks(a.V) * 4 * 16) {
+    // every node and token has a workgroup, the grid is within its limits, and the stretches' parts fit the workspace
+    const int rows = logit_rows(a.C, a.N, a.V), chunks = logit_chunks(a.V);
+    const long long groups = rows > 0 ? (a.N + rows - 1) / rows : 0;
+    if (rows < 1 || rows > a.N || groups * rows < a.N || (long long)chunks * kLogitChunk < a.V || groups > 65535 ||
+        logit_workspace_bytes(a.C, a.N, a.V) != (size_t)a.C * a.N * chunks * (kLogitThreads / 64) * 16) {
         std::printf("plan of C %d N %d V %d\n", a.C, a.N, a.V);
         std::abort();
     }
