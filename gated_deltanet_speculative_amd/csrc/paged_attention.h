@@ -130,16 +130,25 @@ template <int kRowBytes>
 __device__ inline int swizzle(int r) {
     return kRowBytes == 128 ? ((r >> 1) & 3) << 1 : (r & 7) << 1;
 }
-template <int kRowBytes>
+// kTurned: for a 4-bit cache's tile of 16-bit values, whose lanes write several chunks in a row each: eight lanes write at a
+// time, to 32 banks, and would share them two or four at a time, as all are at the same one of their chunks.  So
+// chunks are placed one (and two) further along by the bits of their number (a row of 128 bytes: the row's) that tell
+// those lanes apart; what is read together has the same such bits.  (Without: 8 to 24 cycles more a write, 44% of the LDS time of
+// chunks at D = 256.)
+template <int kRowBytes, bool kTurned = false>
 __device__ inline int lds_at(int r, int chunk) {
-    return r * kRowBytes + ((chunk ^ swizzle<kRowBytes>(r)) << 4);
+    int at = chunk ^ swizzle<kRowBytes>(r);
+    if constexpr (kTurned) at ^= kRowBytes == 512 ? (chunk >> 3) & 3 : kRowBytes == 256 ? (chunk >> 3) & 1 : r & 1;
+    return r * kRowBytes + (at << 4);
 }
+template <typename T, bool kFour = true>
+constexpr bool turned() { return kFour && sizeof(T) == 2; }
 
 // The left operand of the second product: contraction step u (32 cache rows of a 16-bit tile, 16
 // of a 32-bit one) and output columns 16 dt .. 16 dt + 15.  Slot j = 4t + i of lane group g is cache
 // row 32u + 16t + 4g + i (t = 0 only for 32-bit).
 // (kPairs false: 16 cache rows of a 16-bit tile, in the first two words.)
-template <typename T, int D, bool kPairs = true>
+template <typename T, int D, bool kPairs = true, bool kFour = false>
 __device__ inline v4i v_operand(const char *vt, int u, int dt, int lane) {
     constexpr int RB = D * sizeof(T);
     const int g = lane >> 4, n = lane & 15;
@@ -148,7 +157,7 @@ __device__ inline v4i v_operand(const char *vt, int u, int dt, int lane) {
 #pragma unroll
         for (int t = 0; t < (kPairs ? 2 : 1); ++t) {
             const int row = (kPairs ? 32 : 16) * u + 16 * t + 4 * g + (n >> 2);
-            const char *p = vt + lds_at<RB>(row, 2 * dt + ((n & 3) >> 1)) + 8 * (n & 1);
+            const char *p = vt + lds_at<RB, turned<T, kFour>()>(row, 2 * dt + ((n & 3) >> 1)) + 8 * (n & 1);
             part[t] = __builtin_bit_cast(
                 v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
         }
@@ -310,16 +319,21 @@ struct Codes {
         w = *reinterpret_cast<const words *>(static_cast<const char *>(codes) + (size_t)row * (D / 2) + B * part);
         scale = static_cast<const unsigned char *>(scales)[(size_t)row * (D / 32) + B * part / 16];
     }
-    // its values into a tile row of LDS (zeros where the row has no page)
+    // its values into a tile row of LDS
     template <typename T, int D>
-    __device__ void store(char *tile, int r, int part, bool ok) const {
-        constexpr int H = sizeof(T) == 2 ? 1 : 2;  // 16-byte chunks a word of codes
+    __device__ void store(char *tile, int r, int part) const {
+        constexpr int H = sizeof(T) == 2 ? 1 : 2;  // chunks a word of codes
 #pragma unroll
         for (int j = 0; j < B / 4; ++j)
 #pragma unroll
             for (int h = 0; h < H; ++h)
-                *reinterpret_cast<v4i *>(tile + lds_at<D * sizeof(T)>(r, (B / 4 * part + j) * H + h)) =
-                    four_values<T>(ok ? w[j] : 0, ok ? scale : 127u, h);
+                *reinterpret_cast<v4i *>(tile + lds_at<D * sizeof(T), turned<T>()>(r, (B / 4 * part + j) * H + h)) = four_values<T>(w[j], scale, h);
+    }
+    // zeros for a row without a page
+    __device__ void drop(bool ok) {
+#pragma unroll
+        for (int j = 0; j < B / 4; ++j) w[j] = ok ? w[j] : 0;
+        scale = ok ? scale : 127u;
     }
 };
 
@@ -330,6 +344,7 @@ struct FourTile {
     static constexpr int B = TOK * D / 32 >= THREADS ? 16 : 8, PPR = D / 2 / B, ALL = TOK * PPR;
     static constexpr bool kBoth = ALL >= THREADS;
     static constexpr int NP = kBoth ? ALL / THREADS : 1;
+    static constexpr unsigned long long kAll = TOK == 64 ? ~0ull : (1ull << TOK) - 1ull;
     static_assert(kBoth ? ALL % THREADS == 0 : 2 * ALL == THREADS, "");
     Codes<B> k[NP], v[kBoth ? NP : 1];
     template <typename Rows>
@@ -350,19 +365,21 @@ struct FourTile {
                 v[p].template load<D>(a.v_cache, a.v_scales, rows.at(at / PPR), at % PPR);
             }
     }
-    __device__ void store_k(unsigned long long have, char *s_k, char *s_v) const {
+    __device__ void store_k(unsigned long long have, char *s_k, char *s_v) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int at = (int)threadIdx.x % ALL + THREADS * p, r = at / PPR;
-            k[p].template store<T, D>(kBoth || threadIdx.x < ALL ? s_k : s_v, r, at % PPR, (have >> r) & 1);
+            if (have != kAll) k[p].drop((have >> r) & 1);
+            k[p].template store<T, D>(kBoth || threadIdx.x < ALL ? s_k : s_v, r, at % PPR);
         }
     }
-    __device__ void store_v(unsigned long long have, char *s_v) const {
+    __device__ void store_v(unsigned long long have, char *s_v) {
         if constexpr (kBoth)
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 const int at = (int)threadIdx.x + THREADS * p, r = at / PPR;
-                v[p].template store<T, D>(s_v, r, at % PPR, (have >> r) & 1);
+                if (have != kAll) v[p].drop((have >> r) & 1);
+                v[p].template store<T, D>(s_v, r, at % PPR);
             }
     }
 };
@@ -501,7 +518,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &pla
         {
             constexpr int kSteps = NS * NT;  // (contraction outermost: the products of one score tile depend on each other)
             auto operand = [&](int k) {
-                return *reinterpret_cast<const v4i *>(s_k + lds_at<RB>(16 * (k % NT) + (lane & 15), 4 * (k / NT) + g));
+                return *reinterpret_cast<const v4i *>(s_k + lds_at<RB, turned<T, kFour>()>(16 * (k % NT) + (lane & 15), 4 * (k / NT) + g));
             };
             v4i kf[kDeep];
 #pragma unroll
@@ -591,7 +608,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &pla
 #pragma unroll
             for (int e = 0; e < kScores; ++e) weigh(rt, e);
 #pragma unroll
-        for (int k = 0; k < kDeep; ++k) vf[k] = v_operand<T, D>(s_v, k / ND, k % ND, lane);
+        for (int k = 0; k < kDeep; ++k) vf[k] = v_operand<T, D, true, kFour>(s_v, k / ND, k % ND, lane);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             const int u = k / ND, dt = k % ND;
@@ -607,7 +624,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &pla
             if constexpr (kMasked) strange |= drop_nonfinite<T>(vf[k % kDeep]);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) o[rt][dt] = Type<T>::mma(vf[k % kDeep], pf[rt], o[rt][dt]);
-            if (k + kDeep < kSteps) vf[k % kDeep] = v_operand<T, D>(s_v, (k + kDeep) / ND, (k + kDeep) % ND, lane);
+            if (k + kDeep < kSteps) vf[k % kDeep] = v_operand<T, D, true, kFour>(s_v, (k + kDeep) / ND, (k + kDeep) % ND, lane);
             if (u + 1 < NU)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
@@ -640,7 +657,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &pla
                         }
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt) {
-                            const v4i vf = nonfinite_ones<T>(v_operand<T, D>(s_v, u, dt, lane), side);
+                            const v4i vf = nonfinite_ones<T>(v_operand<T, D, true, kFour>(s_v, u, dt, lane), side);
 #pragma unroll
                             for (int rt = 0; rt < RT; ++rt) {
                                 const v4f n = Type<T>::mma(vf, reads[rt], v4f{0.f, 0.f, 0.f, 0.f});
@@ -888,7 +905,7 @@ __device__ __forceinline__ void attn_pair(const AttnArgs &a, const AttnPlan &pla
         if (active) {
             constexpr int kSteps = NS * NT;
             auto operand = [&](int k) {
-                return *reinterpret_cast<const v4i *>(s_k + 32 * hf * RB + lds_at<RB>(16 * (k % NT) + n, 4 * (k / NT) + g));
+                return *reinterpret_cast<const v4i *>(s_k + 32 * hf * RB + lds_at<RB, turned<T, kFour>()>(16 * (k % NT) + n, 4 * (k / NT) + g));
             };
             v4i kf[kDeep];
 #pragma unroll
@@ -993,7 +1010,7 @@ __device__ __forceinline__ void attn_pair(const AttnArgs &a, const AttnPlan &pla
         v4i vf[kDeep], other[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) other[rt] = s_p[pair][hf ^ 1][rt][lane];
-        auto operand = [&](int k) { return v_operand<T, D>(s_v + 32 * RB * (k < ND ? hf : hf ^ 1), 0, 8 * hf + k % ND, lane); };
+        auto operand = [&](int k) { return v_operand<T, D, true, kFour>(s_v + 32 * RB * (k < ND ? hf : hf ^ 1), 0, 8 * hf + k % ND, lane); };
 #pragma unroll
         for (int k = 0; k < kDeep; ++k) vf[k] = operand(k);
 #pragma unroll
@@ -1021,7 +1038,7 @@ __device__ __forceinline__ void attn_pair(const AttnArgs &a, const AttnPlan &pla
                     }
 #pragma unroll
                     for (int dt = 0; dt < ND; ++dt) {
-                        const v4i f = nonfinite_ones<T>(v_operand<T, D>(s_v + 32 * RB * half, 0, 8 * hf + dt, lane), side & 1);
+                        const v4i f = nonfinite_ones<T>(v_operand<T, D, true, kFour>(s_v + 32 * RB * half, 0, 8 * hf + dt, lane), side & 1);
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
                             const v4f cnt = Type<T>::mma(f, reads[rt], v4f{0.f, 0.f, 0.f, 0.f});
@@ -1270,7 +1287,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, const AttnPlan &plan
                 pf = __builtin_bit_cast(v4i, s[u]);
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) {
-                v4i vf = v_operand<T, D, kPairs>(s_v, u, dt, lane);
+                v4i vf = v_operand<T, D, kPairs, kFour>(s_v, u, dt, lane);
                 if constexpr (kMasked) strange |= drop_nonfinite<T>(vf);
                 if constexpr (kPairs || sizeof(T) == 4)
                     o[dt] = Type<T>::mma(vf, pf, o[dt]);
@@ -1296,7 +1313,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, const AttnPlan &plan
                             reads = __builtin_bit_cast(v4i, one[0]);
 #pragma unroll
                         for (int dt = 0; dt < ND; ++dt) {
-                            const v4i vf = nonfinite_ones<T>(v_operand<T, D, kPairs>(s_v, u, dt, lane), side);
+                            const v4i vf = nonfinite_ones<T>(v_operand<T, D, kPairs, kFour>(s_v, u, dt, lane), side);
                             v4f cnt{0.f, 0.f, 0.f, 0.f};
                             if constexpr (kPairs || sizeof(T) == 4)
                                 cnt = Type<T>::mma(vf, reads, cnt);
@@ -1343,7 +1360,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs &a, const AttnPlan &plan
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     const int r = RPP * p + lane / (D / 32);
-                    vc[p].template store<T, D>(s_v, r, lane % (D / 32), (here >> r) & 1);
+                    if (here != kFull) vc[p].drop((here >> r) & 1);
+                    vc[p].template store<T, D>(s_v, r, lane % (D / 32));
                 }
             } else {
 #pragma unroll
