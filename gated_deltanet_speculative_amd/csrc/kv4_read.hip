@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 16;  // tokens of a workgroup
+constexpr int kAhead = 4;     // rows of a thread that are requested together
 
 template <typename T>
 __device__ inline void four_out(T *p, int w, unsigned scale) {
@@ -33,13 +34,14 @@ __device__ inline void four_out(T *p, int w, unsigned scale) {
     }
 }
 
-// Grid: (tokens / kTokens, lanes, layers), K and V one after the other.
+// Grid: (tokens / kTokens, lanes, 2 layers + (K or V)).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(AttnDims d, Cache4Layers cl, PagedLanes l,
                                                             const int32_t *__restrict__ first_row, T *__restrict__ k_out,
                                                             T *__restrict__ v_out) {
-    __shared__ int s_row[kTokens];  // cache row of a token for kv head 0, -1 without a page
-    const int tid = threadIdx.x, c = blockIdx.y, layer = blockIdx.z, i0 = blockIdx.x * kTokens;
+    constexpr int LPR = D / 8, kStep = kThreads / LPR;  // lanes a row, rows a round
+    __shared__ int s_row[kTokens];                      // cache row of a token for kv head 0, -1 without a page
+    const int tid = threadIdx.x, c = blockIdx.y, layer = blockIdx.z >> 1, side = blockIdx.z & 1, i0 = blockIdx.x * kTokens;
     const int slot = l.slot_ids[c], nodes = l.lane_nodes ? l.lane_nodes[c] : d.N, first = first_row[c];
     if (slot == -1) return;
     int bits = 0;
@@ -47,7 +49,7 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(AttnDims d, Cache4La
     if (slot < -1 || slot >= d.P) bits |= GDN_STATUS_SLOT_RANGE;
     if (first < 0 || (int64_t)first + max(nodes, 0) > (int64_t)d.max_pages * d.page.d) bits |= GDN_STATUS_LENGTH;
     if (bits) {
-        if (tid == 0 && i0 == 0 && layer == 0 && l.status) atomicOr(l.status, bits);
+        if (tid == 0 && i0 == 0 && blockIdx.z == 0 && l.status) atomicOr(l.status, bits);
         return;
     }
     const int n = min(nodes - i0, kTokens);
@@ -57,29 +59,42 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(AttnDims d, Cache4La
         const int pid = l.page_table[(int64_t)slot * d.max_pages + entry];
         const bool paged = (unsigned)pid < (unsigned)d.n_pages;
         s_row[tid] = paged ? (int)cache_row(d, pid, 0, t, entry) : -1;
-        if (!paged && layer == 0 && l.status) atomicOr(l.status, GDN_STATUS_PAGE);
+        if (!paged && blockIdx.z == 0 && l.status) atomicOr(l.status, GDN_STATUS_PAGE);
     }
+    T *out = side ? v_out : k_out;
+    if (!out) return;
     lds_barrier();
-    constexpr int LPR = D / 8;  // lanes a row
-    const size_t out0 = (((size_t)layer * d.C + c) * d.N + i0) * d.Hkv;
-    for (int side = 0; side < 2; ++side) {
-        T *out = side ? v_out : k_out;
-        if (!out) continue;
-        const int *codes = static_cast<const int *>(side ? cl.codes.v[layer] : cl.codes.k[layer]);
-        const unsigned char *scales = static_cast<const unsigned char *>(side ? cl.scales.v[layer] : cl.scales.k[layer]);
-        for (int k = tid; k < n * d.Hkv * LPR; k += kThreads) {
-            const int sub = k % LPR, r = k / LPR, i = r / d.Hkv, h = r - i * d.Hkv;
-            if (s_row[i] < 0) continue;
-            const size_t row = (size_t)s_row[i] + (size_t)h * d.page.d;
-            four_out<T>(out + (out0 + r) * D + 8 * sub, codes[row * LPR + sub], scales[row * (D / 32) + sub / 4]);
+    const int *codes = static_cast<const int *>(side ? cl.codes.v[layer] : cl.codes.k[layer]);
+    const unsigned char *scales = static_cast<const unsigned char *>(side ? cl.scales.v[layer] : cl.scales.k[layer]);
+    out += (((size_t)layer * d.C + c) * d.N + i0) * d.Hkv * D;
+    // this thread's rows (token, head), kStep apart
+    const int sub = tid % LPR, rows = n * d.Hkv, step_i = kStep / d.Hkv, step_h = kStep - step_i * d.Hkv;
+    int r = tid / LPR, i = r / d.Hkv, h = r - i * d.Hkv;
+    while (r < rows) {
+        int w[kAhead], at[kAhead];
+        unsigned s[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int row = r < rows ? s_row[i] : -1;
+            at[j] = row < 0 ? -1 : r;
+            const size_t from = (size_t)max(row, 0) + (size_t)(row < 0 ? 0 : h) * d.page.d;
+            w[j] = codes[from * LPR + sub];
+            s[j] = scales[from * (D / 32) + sub / 4];
+            r += kStep;
+            i += step_i;
+            h += step_h;
+            if (h >= d.Hkv) h -= d.Hkv, ++i;
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (at[j] >= 0) four_out<T>(out + (size_t)at[j] * D + 8 * sub, w[j], s[j]);
     }
 }
 
 template <typename T>
 hipError_t launch(const AttnDims &d, int n_layers, const Cache4Layers &cl, const PagedLanes &l, const int32_t *first_row,
                   void *k_out, void *v_out, hipStream_t stream) {
-    const dim3 grid((d.N + kTokens - 1) / kTokens, d.C, n_layers);
+    const dim3 grid((d.N + kTokens - 1) / kTokens, d.C, 2 * n_layers);
     T *k = static_cast<T *>(k_out), *v = static_cast<T *>(v_out);
     if (d.D == 64)
         hipLaunchKernelGGL((kv4_read_kernel<T, 64>), grid, dim3(kThreads), 0, stream, d, cl, l, first_row, k, v);

@@ -69,8 +69,8 @@ __device__ inline Quantised quantised(const float (&x)[8]) {
     unsigned m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-    m = max(m, (unsigned)__shfl_xor((int)m, 1));
-    m = max(m, (unsigned)__shfl_xor((int)m, 2));
+    m = max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));  // lane ^ 1
+    m = max(m, (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, false));  // lane ^ 2
     if (m >= 0x7f800000u) return Quantised{0, 255u};
     const unsigned scale = (unsigned)min(max((int)((m + 0x200000u) >> 23) - 2, 2), kMost);
     const float s = __uint_as_float(scale << 23);
@@ -190,7 +190,8 @@ __device__ __forceinline__ void rope_kv_write(const RopeArgs &a) {
                     }
                 }
                 Quantised four{};
-                if constexpr (kFour) four = quantised<T>(x);
+                if constexpr (kFour)
+                    if (__builtin_amdgcn_ballot_w64(kind > 0)) four = quantised<T>(x);
                 if (!has) continue;
                 if (kind == 0) {
                     store8(static_cast<T *>(a.q_out) + (node * d.Hq + h) * D + 8 * sub, x);
@@ -213,8 +214,9 @@ template <typename X, typename T, int D>
 __global__ __launch_bounds__(kThreads) void rope_kv_write_kernel(RopeArgs a) {
     rope_kv_write<X, T, D, false>(a);
 }
+// (four workgroups a CU, as the other has by itself: with 141 registers instead of 128, 2 x 4096 tokens took 94 us)
 template <typename X, typename T, int D>
-__global__ __launch_bounds__(kThreads) void rope_kv4_write_kernel(RopeArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void rope_kv4_write_kernel(RopeArgs a) {
     rope_kv_write<X, T, D, true>(a);
 }
 
