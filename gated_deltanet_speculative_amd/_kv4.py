@@ -1,20 +1,20 @@
-"""ctypes binding of the gdn_kv4.h calls: the attention layers' part of a round over a cache held in 4 bits.
+"""Binding of the gdn_kv4.h calls: the attention layers' part of a round over a cache held in 4 bits.
 
-Argument marshalling only, as in the binding of the gdn_round.h calls, whose helpers and shapes it uses.  There is no
-fallback.
+Argument marshalling only: missing outputs are allocated here, the tensors are checked and the calls made by the binding's
+extension (csrc/marshal.cpp).  There is no fallback.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
-import struct
 from typing import NamedTuple
 
 import torch
 
 from . import _round as R
-from ._lib import MAX_LAYERS, load_library
+from ._lib import load_library
 
 KV4_EXPORTED = ("gdn_rope_kv4_write", "gdn_paged_attention_kv4", "gdn_paged_attention_kv4_workspace_size",
                 "gdn_kv4_commit_layers", "gdn_kv4_read_layers")
@@ -40,53 +40,33 @@ def kv4_cache(sh: R.AttnShape, device="cuda", layers=None) -> Kv4Cache:
     return Kv4Cache(make(0, 2), make(127, 32), make(0, 2), make(127, 32))
 
 
-_calls = None
-
-
+@functools.lru_cache(maxsize=1)
 def _library():
-    """The library with the prototypes of these calls (looked up once)."""
-    global _calls
-    if _calls is None:
-        lib = load_library()
-        sp = ctypes.POINTER(R._CAttnShape)
-        lib.gdn_rope_kv4_write.argtypes = [sp, _i32, _vp, _vp, _vp, ctypes.POINTER(R._CRope)] + [_vp] * 9
-        lib.gdn_paged_attention_kv4.argtypes = [sp] + [_vp] * 7 + [ctypes.c_float, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]
-        lib.gdn_paged_attention_kv4_workspace_size.argtypes = [sp]
-        lib.gdn_kv4_commit_layers.argtypes = [sp, _i32] + [_vp] * 10
-        lib.gdn_kv4_read_layers.argtypes = [sp, _i32] + [_vp] * 9
-        for f in ("gdn_rope_kv4_write", "gdn_paged_attention_kv4", "gdn_kv4_commit_layers", "gdn_kv4_read_layers"):
-            getattr(lib, f).restype = _i32
-        lib.gdn_paged_attention_kv4_workspace_size.restype = ctypes.c_size_t
-        _calls = lib
-    return _calls
+    """The library with the prototypes of these calls."""
+    lib = load_library()
+    sp = ctypes.POINTER(R._CAttnShape)
+    lib.gdn_rope_kv4_write.argtypes = [sp, _i32, _vp, _vp, _vp, ctypes.POINTER(R._CRope)] + [_vp] * 9
+    lib.gdn_paged_attention_kv4.argtypes = [sp] + [_vp] * 7 + [ctypes.c_float, _vp, _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+    lib.gdn_paged_attention_kv4_workspace_size.argtypes = [sp]
+    lib.gdn_kv4_commit_layers.argtypes = [sp, _i32] + [_vp] * 10
+    lib.gdn_kv4_read_layers.argtypes = [sp, _i32] + [_vp] * 9
+    for f in ("gdn_rope_kv4_write", "gdn_paged_attention_kv4", "gdn_kv4_commit_layers", "gdn_kv4_read_layers"):
+        getattr(lib, f).restype = _i32
+    lib.gdn_paged_attention_kv4_workspace_size.restype = ctypes.c_size_t
+    return lib
 
 
-_four = struct.Struct("4P").pack
+@functools.lru_cache(maxsize=None)
+def _call_of(name: str) -> tuple:
+    """The extension's function that makes a call, and the call's address in the library."""
+    return getattr(R._load_marshal(), name), ctypes.cast(getattr(_library(), "gdn_" + name), _vp).value
 
 
-def _pointers(cache, sh, device, lead=()) -> list:
-    """Addresses of the four tensors of a Kv4Cache, in the order of gdn_kv4_cache."""
-    if not isinstance(cache, Kv4Cache):
-        raise TypeError("the cache must be a Kv4Cache")
-    codes = (*lead, sh.n_pages, sh.n_kv_heads, sh.page_size, sh.head_dim // 2)
-    scales = (*codes[:-1], sh.head_dim // 32)
-    return [R._ptr(cache.k, "cache.k", torch.uint8, codes, device), R._ptr(cache.k_scale, "cache.k_scale", torch.uint8, scales, device),
-            R._ptr(cache.v, "cache.v", torch.uint8, codes, device), R._ptr(cache.v_scale, "cache.v_scale", torch.uint8, scales, device)]
-
-
-def _layers(caches, sh, device, name) -> tuple:
-    """(number of layers, gdn_kv4_cache array as bytes) of one Kv4Cache with a leading layer axis, or of a sequence."""
-    if isinstance(caches, Kv4Cache):
-        n = caches.k.shape[0] if isinstance(caches.k, torch.Tensor) and caches.k.dim() else 0
-        step = sh.n_pages * sh.n_kv_heads * sh.page_size * sh.head_dim
-        base = _pointers(caches, sh, device, (n,)) if n else []
-        flat = [p + i * (step // (32 if j % 2 else 2)) for i in range(n) for j, p in enumerate(base)]
-    else:
-        flat = [p for c in caches for p in _pointers(c, sh, device)]
-        n = len(flat) // 4
-    if not 1 <= n <= MAX_LAYERS:
-        raise ValueError(f"{name}: {n} layers, expected 1..{MAX_LAYERS}")
-    return n, struct.pack(f"{4 * n}P", *flat)
+@functools.lru_cache(maxsize=256)
+def _shape(sh) -> tuple:
+    """A shape's C struct (never written to), and its address."""
+    cs = sh.c_struct()
+    return cs, ctypes.addressof(cs)
 
 
 def rope_kv4_write(sh: R.AttnShape, q, k, v, inv_freq, cache, slot_ids, page_table, seq_len, positions=None, pair_axis=None,
@@ -95,15 +75,19 @@ def rope_kv4_write(sh: R.AttnShape, q, k, v, inv_freq, cache, slot_ids, page_tab
     """Rotary positions of q and k and the write of k and v, quantised to 4 bits, into the slots' pages behind their
     committed rows: rope_kv_write with a Kv4Cache in the place of the two caches.  Returns (q_out, status)."""
     device = R._device(q, "q")
-    q_out, status, lead, tail = R._rope_arguments(sh, q, k, v, inv_freq, slot_ids, page_table, seq_len, positions, pair_axis,
-                                                  parents, lane_nodes, q_norm, k_norm, eps, interleaved, q_out, status, device)
-    R._call(device, _library().gdn_rope_kv4_write, "gdn_rope_kv4_write", *lead, _four(*_pointers(cache, sh, device)), *tail)
+    call, f = _call_of("rope_kv4_write")
+    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    if q_out is None:
+        q_out = torch.empty((sh.n_seqs, sh.n_nodes, sh.n_q_heads, sh.head_dim), dtype=sh.dtype, device=device)
+    status = R._status_word(status, device)
+    R._call(device, call, "gdn_rope_kv4_write", f, shape, device, q, k, v, inv_freq, cache, slot_ids,
+            page_table, seq_len, positions, pair_axis, parents, lane_nodes, q_norm, k_norm, eps, bool(interleaved), q_out, status)
     return q_out, status
 
 
 def paged_attention_kv4_workspace_size(sh: R.AttnShape) -> int:
     """Bytes of device workspace paged_attention_kv4 needs for this shape (0 for an invalid shape)."""
-    return int(_library().gdn_paged_attention_kv4_workspace_size(ctypes.byref(R._cs(sh))))
+    return int(_library().gdn_paged_attention_kv4_workspace_size(ctypes.byref(_shape(sh)[0])))
 
 
 def paged_attention_kv4(sh: R.AttnShape, q, cache, slot_ids, page_table, seq_len, parents=None, lane_nodes=None, scale=None,
@@ -111,20 +95,16 @@ def paged_attention_kv4(sh: R.AttnShape, q, cache, slot_ids, page_table, seq_len
     """Attention of the round's tokens over a 4-bit cache: paged_attention with a Kv4Cache in the place of the two
     caches (`workspace` is at least paged_attention_kv4_workspace_size(sh) bytes).  Returns (out, status)."""
     device = R._device(q, "q")
-    shape = (sh.n_seqs, sh.n_nodes, sh.n_q_heads, sh.head_dim)
+    call, f = _call_of("paged_attention_kv4")
+    held, shape = _shape(sh)  # (held: the struct lives through the call)
     if out is None:
-        out = torch.empty(shape, dtype=sh.dtype, device=device)
+        out = torch.empty((sh.n_seqs, sh.n_nodes, sh.n_q_heads, sh.head_dim), dtype=sh.dtype, device=device)
     status = R._status_word(status, device)
-    lib, cs = _library(), ctypes.byref(R._cs(sh))
     if workspace is None:
-        workspace = torch.empty(max(lib.gdn_paged_attention_kv4_workspace_size(cs) // 4, 1), dtype=torch.float32, device=device)
-    else:
-        workspace = R._scratch(workspace, device)
-    R._call(device, lib.gdn_paged_attention_kv4, "gdn_paged_attention_kv4", cs, R._ptr(q, "q", sh.dtype, shape, device),
-            _four(*_pointers(cache, sh, device)), *R._places(sh, slot_ids, page_table, seq_len, device),
-            *R._tree(sh, parents, lane_nodes, device), 1.0 / math.sqrt(sh.head_dim) if scale is None else scale,
-            None if gate is None else R._view(gate, "gate", sh.dtype, shape, device), int(gate_mode),
-            R._ptr(out, "out", sh.dtype, shape, device), workspace.data_ptr(), workspace.numel() * 4, status.data_ptr())
+        workspace = torch.empty(max(paged_attention_kv4_workspace_size(sh) // 4, 1), dtype=torch.float32, device=device)
+    R._call(device, call, "gdn_paged_attention_kv4", f, shape, device, q, cache, slot_ids, page_table,
+            seq_len, parents, lane_nodes, 1.0 / math.sqrt(sh.head_dim) if scale is None else scale, gate, int(gate_mode), out,
+            workspace, status)
     return out, status
 
 
@@ -136,14 +116,12 @@ def kv4_commit_layers(sh: R.AttnShape, caches, slot_ids, page_table, seq_len, ac
     if status is None:
         raise ValueError("kv4_commit_layers needs a status word (the round's transaction flag)")
     device = R._device(status, "status")
+    call, f = _call_of("kv4_commit_layers")
+    held, shape = _shape(sh)  # (held: the struct lives through the call)
     if new_len is None:
         new_len = torch.empty(sh.n_slots, dtype=torch.int32, device=device)
-    n, arrays = _layers(caches, sh, device, "kv4_commit_layers")
-    R._call(device, _library().gdn_kv4_commit_layers, "gdn_kv4_commit_layers", ctypes.byref(R._cs(sh)), n, arrays,
-            *R._places(sh, slot_ids, page_table, seq_len, device), *R._tree(sh, parents, lane_nodes, device),
-            R._ptr(accept_node, "accept_node", torch.int32, (sh.n_seqs,), device),
-            R._ptr(new_len, "new_len", torch.int32, (sh.n_slots,), device),
-            R._ptr(status, "status", torch.int32, (1,), device))
+    R._call(device, call, "gdn_kv4_commit_layers", f, shape, device, caches, slot_ids, page_table,
+            seq_len, parents, lane_nodes, accept_node, new_len, status)
     return new_len
 
 
@@ -153,14 +131,13 @@ def kv4_read_layers(sh: R.AttnShape, caches, slot_ids, page_table, first_row, la
     kv4_commit_layers).  Returns (k_out, v_out [layers, C, N, H_kv, D], status); rows that are absent (lane_nodes),
     of an offending lane or in a page outside the pool keep what k_out and v_out held (zeros if they are not given)."""
     device = R._device(slot_ids, "slot_ids")
-    n, arrays = _layers(caches, sh, device, "kv4_read_layers")
-    shape = (n, sh.n_seqs, sh.n_nodes, sh.n_kv_heads, sh.head_dim)
-    k_out, v_out = (torch.zeros(shape, dtype=sh.dtype, device=device) if t is None else t for t in (k_out, v_out))
+    call, f = _call_of("kv4_read_layers")
+    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    if k_out is None or v_out is None:
+        n = caches.k.shape[0] if isinstance(caches, Kv4Cache) else len(caches)
+        rows = (n, sh.n_seqs, sh.n_nodes, sh.n_kv_heads, sh.head_dim)
+        k_out, v_out = (torch.zeros(rows, dtype=sh.dtype, device=device) if t is None else t for t in (k_out, v_out))
     status = R._status_word(status, device)
-    R._call(device, _library().gdn_kv4_read_layers, "gdn_kv4_read_layers", ctypes.byref(R._cs(sh)), n, arrays,
-            R._ptr(slot_ids, "slot_ids", torch.int32, (sh.n_seqs,), device),
-            R._ptr(page_table, "page_table", torch.int32, (sh.n_slots, sh.max_pages), device),
-            R._ptr(first_row, "first_row", torch.int32, (sh.n_seqs,), device),
-            R._opt(lane_nodes, "lane_nodes", torch.int32, (sh.n_seqs,), device),
-            R._ptr(k_out, "k_out", sh.dtype, shape, device), R._ptr(v_out, "v_out", sh.dtype, shape, device), status.data_ptr())
+    R._call(device, call, "gdn_kv4_read_layers", f, shape, device, caches, slot_ids, page_table, first_row,
+            lane_nodes, k_out, v_out, status)
     return k_out, v_out, status

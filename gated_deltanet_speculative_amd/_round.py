@@ -125,7 +125,7 @@ def _view(*args):
     return _view(*args)
 
 
-def _load_marshal() -> None:
+def _load_marshal():
     global _ptr, _opt, _view
     try:
         from . import _marshal
@@ -133,6 +133,7 @@ def _load_marshal() -> None:
         raise RuntimeError("_marshal.so is missing: build it with `python -m gated_deltanet_speculative_amd.build`") from e
     _marshal.init(_refuse)
     _ptr, _opt, _view = _marshal.ptr, _marshal.opt, _marshal.view
+    return _marshal
 
 
 def _refuse(t, name, dtype, shape, device):
@@ -206,16 +207,6 @@ def rope_kv_write(sh: AttnShape, q, k, v, inv_freq, k_cache, v_cache, slot_ids, 
     k_norm are float32 [D].  Returns (q_out [C, N, H_q, D], status).
     """
     device = _device(q, "q")
-    q_out, status, lead, tail = _rope_arguments(sh, q, k, v, inv_freq, slot_ids, page_table, seq_len, positions, pair_axis,
-                                                parents, lane_nodes, q_norm, k_norm, eps, interleaved, q_out, status, device)
-    _call(device, _library().gdn_rope_kv_write, "gdn_rope_kv_write", *lead, _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
-          _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *tail)
-    return q_out, status
-
-
-def _rope_arguments(sh, q, k, v, inv_freq, slot_ids, page_table, seq_len, positions, pair_axis, parents, lane_nodes, q_norm,
-                    k_norm, eps, interleaved, q_out, status, device) -> tuple:
-    """q_out, status, and the arguments of a rotary cache write in front of the cache's and behind them."""
     C, N, D = sh.n_seqs, sh.n_nodes, sh.head_dim
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a one-dimensional float64 tensor of rot_dim / 2 entries")
@@ -235,11 +226,13 @@ def _rope_arguments(sh, q, k, v, inv_freq, slot_ids, page_table, seq_len, positi
                   _opt(pair_axis, "pair_axis", torch.int32, (half,), device), n_axes, 2 * half, int(bool(interleaved)),
                   _opt(q_norm, "q_norm", torch.float32, (D,), device),
                   _opt(k_norm, "k_norm", torch.float32, (D,), device), eps)
-    lead = (ctypes.byref(_cs(sh)), _dtype_code(x), _view(q, "q", x, q_shape, device), _view(k, "k", x, kv_shape, device),
-            _view(v, "v", x, kv_shape, device), ctypes.byref(rope))
-    tail = (*_places(sh, slot_ids, page_table, seq_len, device), *_tree(sh, parents, lane_nodes, device),
-            _ptr(q_out, "q_out", sh.dtype, q_shape, device), status.data_ptr())
-    return q_out, status, lead, tail
+    _call(device, _library().gdn_rope_kv_write, "gdn_rope_kv_write", ctypes.byref(_cs(sh)), _dtype_code(x),
+          _view(q, "q", x, q_shape, device), _view(k, "k", x, kv_shape, device), _view(v, "v", x, kv_shape, device),
+          ctypes.byref(rope), _ptr(k_cache, "k_cache", sh.dtype, sh.cache_shape, device),
+          _ptr(v_cache, "v_cache", sh.dtype, sh.cache_shape, device), *_places(sh, slot_ids, page_table, seq_len, device),
+          *_tree(sh, parents, lane_nodes, device),
+          _ptr(q_out, "q_out", sh.dtype, q_shape, device), status.data_ptr())
+    return q_out, status
 
 
 def paged_attention_workspace_size(sh: AttnShape) -> int:

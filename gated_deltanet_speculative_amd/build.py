@@ -5,7 +5,7 @@
 Compiles every source under csrc/ to an object in _build/ and links the shared
 library next to this file, and beside it the Python binding's tensor checks (_marshal.so),
 unless --library is given.  Always recompiles (cheap: a few seconds per file).  The library
-needs hipcc alone; the tensor checks need g++ and the headers of Python and torch.
+needs hipcc alone; the tensor checks need g++ and the headers of Python, torch and HIP.
 """
 
 from __future__ import annotations
@@ -68,7 +68,9 @@ def _build_marshal() -> str:
     import torch
     from torch.utils import cpp_extension as ext
 
-    includes = [a for d in (*ext.include_paths(), sysconfig.get_paths()["include"]) for a in ("-isystem", d)]
+    hip = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")  # (the stream's type, in the library's headers)
+    includes = [a for d in (*ext.include_paths(), sysconfig.get_paths()["include"], hip) for a in ("-isystem", d)]
+    includes += ["-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include")]
     libs = [a for d in ext.library_paths() for a in (f"-L{d}", f"-Wl,-rpath,{d}")]
     tmp = MARSHAL + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

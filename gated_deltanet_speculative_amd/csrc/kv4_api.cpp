@@ -1,5 +1,7 @@
 // Host entry points of gdn_kv4.h: argument validation, byte-range alias checks and kernel dispatch on the caller's stream.
 // Every check runs before anything is enqueued; no entry point allocates, synchronises or keeps state between calls.
+#include <algorithm>
+
 #include "gdn_kv4.h"
 #include "round_checks.h"
 
@@ -26,6 +28,21 @@ int check_layers(const gdn::AttnDims &d, int32_t n_layers, const gdn_kv4_cache *
 Range array_of(const gdn::AttnDims &d, const gdn_kv4_cache &c, int j) {
     const CacheArrays a = arrays_of(c);
     return j & 1 ? a.scales(d, j >> 1) : a.codes(d, j >> 1);
+}
+
+bool overlap_any(const Range &o, std::initializer_list<Range> others) {
+    for (const Range &r : others)
+        if (overlap(o, r)) return true;
+    return false;
+}
+// Whether two of the ranges (none of them empty) overlap: in the order of their addresses, some neighbours then do
+bool any_overlap(const Range *r, int n) {
+    Range by[4 * GDN_MAX_LAYERS];
+    std::copy(r, r + n, by);
+    std::sort(by, by + n, [](const Range &a, const Range &b) { return a.p < b.p; });
+    for (int k = 1; k < n; ++k)
+        if (overlap(by[k - 1], by[k])) return true;
+    return false;
 }
 
 }  // namespace
@@ -82,12 +99,12 @@ int gdn_kv4_commit_layers(const gdn_attn_shape *sh, int32_t n_layers, const gdn_
                                               {lane_nodes, (size_t)d.C * I}, {accept_node, (size_t)d.C * I}};
     if (any_alias({{new_len, (size_t)d.P * I}, {status, I}}, ins)) return GDN_ERR_ALIAS;
     // every array against every input, the other outputs and every other array
-    for (int l = 0; l < 4 * n_layers; ++l) {
-        const Range o = array_of(d, caches[l / 4], l % 4);
-        if (any_alias({o, {new_len, (size_t)d.P * I}, {status, I}}, ins)) return GDN_ERR_ALIAS;
-        for (int m = 0; m < l; ++m)
-            if (overlap(o, array_of(d, caches[m / 4], m % 4))) return GDN_ERR_ALIAS;
-    }
+    Range arrays[4 * GDN_MAX_LAYERS];
+    for (int l = 0; l < 4 * n_layers; ++l) arrays[l] = array_of(d, caches[l / 4], l % 4);
+    if (any_overlap(arrays, 4 * n_layers)) return GDN_ERR_ALIAS;
+    for (int l = 0; l < 4 * n_layers; ++l)
+        if (overlap_any(arrays[l], ins) || overlap(arrays[l], {new_len, (size_t)d.P * I}) || overlap(arrays[l], {status, I}))
+            return GDN_ERR_ALIAS;
     return gdn::launch_kv4_commit(d, n_layers, cl,
                                   gdn::PagedLanes{slot_ids, page_table, seq_len, parents, lane_nodes, status},
                                   accept_node, new_len, stream) == hipSuccess
