@@ -63,14 +63,23 @@ hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
 
 }  // namespace
 
-// As attn_plan; few query rows take the kernel for few in every type, as its tiles of K are codes.
+// As attn_plan, but for two things.  Up to 16 query rows take the kernel for few in every type, float32 rows of 1024 bytes
+// too: its tiles of K are codes, of the same size for all types.  And workgroups of four waves, two of which fill a CU, are
+// divided into one for each CU instead where they would have no more than 256 cache rows: what a workgroup does before and
+// after its tiles then costs more than the second one hides (trees of 16 nodes, 4 heads each, 8 kv heads of 128, bfloat16,
+// with two and with one: a lane at 8192 tokens 22.6 us and 18.5, three at 3000 22.1 and 18.4, four at 2000 19.0 and 17.5,
+// eight at 1000 20.0 and 17.8, twelve at 1000 22.2 and 22.8; but four at 8192, 512 rows, 29.0 and 31.7).
 AttnPlan attn_plan_kv4(const AttnDims &d) {
     const int row_bytes = d.D * (d.dtype == GDN_DTYPE_F32 ? 4 : 2);
-    const int64_t rows = (int64_t)d.N * d.G;
-    if (rows > kFewRows) return attn_plan(d);
+    const int64_t rows = (int64_t)d.N * d.G, held = (int64_t)d.max_pages * d.page.d, groups = (int64_t)d.C * d.Hkv;
+    if (rows > kFewRows) {
+        AttnPlan p = attn_plan(d);
+        if (p.rows_per_group == 64 && d.dtype != GDN_DTYPE_F32 && held <= 256 * p.splits)
+            p.splits = (int)std::min<int64_t>(p.splits, std::max<int64_t>(256 / groups, 1));
+        return p;
+    }
     AttnPlan p{kFewRows, 1, 1};
-    const int64_t groups = (int64_t)d.C * d.Hkv, least = few_tile(row_bytes, true) * kFewWaves, held = (int64_t)d.max_pages * d.page.d;
-    const int64_t most = std::min<int64_t>((held + least - 1) / least, 64), round = 512;
+    const int64_t least = few_tile(row_bytes, true) * kFewWaves, most = std::min<int64_t>((held + least - 1) / least, 64), round = 512;
     p.splits = (int)std::min<int64_t>(most, groups < round ? round / groups : 1);
     return p;
 }
