@@ -65,12 +65,14 @@ __device__ inline float wave_sum(float x) {
     return (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
 }
 constexpr int kAhead = 4;  // loads of a thread that are requested together
-// log2(e) / T within the normal numbers: finite for T = 0, and never 0, so that -infinity times it is -infinity
-__device__ inline float per_temperature(float temp) { return fminf(fmaxf(1.4426950408889634f / temp, 0x1p-126f), 3.4e38f); }
-// e^{(z - m) / T} with k = log2(e) / T; 1 at the maximum even where that is infinite, 0 for -infinity
+// 2 log2(e) / T, finite for T = 0; never 0 (2^-127 for the largest T: not a normal number, but exact to 2^-22), so that
+// -infinity times it is -infinity.  It multiplies half of z - m, which no two finite numbers carry out of range.
+__device__ inline float per_temperature(float temp) { return fminf(2.8853900817779268f / temp, 3.4e38f); }
+__device__ inline float half_below(float z, float half_m) { return fmaf(z, 0.5f, -half_m); }
+// e^{(z - m) / T} with k = 2 log2(e) / T; 1 at the maximum even where that is infinite, 0 for -infinity
 __device__ inline float weight(float z, float m, float k) {
     const float top = m == kNegInf ? 0.f : m;
-    return __builtin_amdgcn_exp2f(z == top ? 0.f : (z - top) * k);
+    return __builtin_amdgcn_exp2f(z == top ? 0.f : half_below(z, 0.5f * top) * k);
 }
 
 // Entries of a slot's history from k0 on, four at a time: entry 4 (j kThreads + tid) + k0 and the next three, or, where
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
         if (a.r.temperature) temp = a.r.temperature[slot];
         if (a.r.history) held = a.r.history_len[slot];
         if (a.r.history && a.r.prompt_len) prompt = a.r.prompt_len[slot];
-        if (!(rep > 0.f) || !__builtin_isfinite(rep) || !__builtin_isfinite(pres) || !__builtin_isfinite(freq) || !(temp >= 0.f) ||
+        if (!(rep >= 0x1p-126f && rep <= 0x1p126f) || !__builtin_isfinite(pres) || !__builtin_isfinite(freq) || !(temp >= 0.f) ||
             !__builtin_isfinite(temp))
             bits |= GDN_STATUS_RULE;
         if (held < 0 || held > a.H || prompt < 0 || prompt > held) bits |= GDN_STATUS_LENGTH;
@@ -390,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
             float sum = 0.f;
             if (fabsf(top.v) < __builtin_inff()) {
 #pragma unroll
-                for (int q = 0; q < W; ++q) sum += __builtin_amdgcn_exp2f((z[q] - top.v) * k2);
+                for (int q = 0; q < W; ++q) sum += __builtin_amdgcn_exp2f(half_below(z[q], 0.5f * top.v) * k2);
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q) sum += weight(z[q], top.v, k2);
@@ -405,7 +407,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
                 const float scale = t.sum == 0.f ? 0.f : 1.f / t.sum;
                 if (temp > 0.f && fabsf(t.top) < __builtin_inff()) {
 #pragma unroll
-                    for (int q = 0; q < W; ++q) z[q] = __builtin_amdgcn_exp2f((z[q] - t.top) * k2) * scale;
+                    for (int q = 0; q < W; ++q) z[q] = __builtin_amdgcn_exp2f(half_below(z[q], 0.5f * t.top) * k2) * scale;
                 } else {
                     const int best = t.top == kNegInf ? -1 : t.at;
 #pragma unroll

@@ -23,8 +23,9 @@ extern "C" {
 #endif
 
 /* A device status bit, next to those of gdn_verify.h and gdn_round.h. */
-#define GDN_STATUS_RULE 512 /* repetition not > 0, or a repetition, presence, frequency or
-                               temperature that is not finite, or a temperature below 0     */
+#define GDN_STATUS_RULE 512 /* repetition outside [2^-126, 2^126] (it and its reciprocal are
+                               normal numbers there), a presence, frequency or temperature
+                               that is not finite, or a temperature below 0                 */
 
 /* Shape errors (GDN_ERR_SHAPE): a non-positive n_seqs, n_nodes, n_slots or vocab, a negative
    max_history or max_bias, an unknown dtype.  GDN_ERR_UNSUPPORTED: C > GDN_MAX_SEQS,
@@ -46,9 +47,9 @@ typedef struct gdn_logit_rules {
     const int32_t *history;     /* [P][max_history] token ids; those outside [0, V) count nowhere */
     const int32_t *history_len; /* [P] entries in use; needed with history (GDN_ERR_NULL)         */
     const int32_t *prompt_len;  /* [P] the first entries that are the prompt's; NULL: none        */
-    const float *repetition;    /* [P] r > 0;  NULL: 1 */
-    const float *presence;      /* [P] p;      NULL: 0 */
-    const float *frequency;     /* [P] f;      NULL: 0 */
+    const float *repetition;    /* [P] r in [2^-126, 2^126]; NULL: 1 */
+    const float *presence;      /* [P] p; NULL: 0 */
+    const float *frequency;     /* [P] f; NULL: 0 */
     const int32_t *bias_tokens; /* [P][max_bias] token ids; those outside [0, V) are skipped      */
     const float *bias;          /* [P][max_bias]; both or neither (GDN_ERR_NULL)                  */
     const float *temperature;   /* [P] T >= 0; NULL: out is the logits                            */

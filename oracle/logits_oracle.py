@@ -21,7 +21,7 @@ def lane_bits(c, N, V, slot_ids, max_history, rules, tokens, parents, lane_nodes
     else:
         for name in ("repetition", "presence", "frequency", "temperature"):
             v = rules.get(name)
-            if v is not None and (not np.isfinite(v[s]) or (name == "repetition" and not v[s] > 0) or (name == "temperature" and v[s] < 0)):
+            if v is not None and (not np.isfinite(v[s]) or (name == "repetition" and not 2.0 ** -126 <= v[s] <= 2.0 ** 126) or (name == "temperature" and v[s] < 0)):
                 bits |= RULE
         if rules.get("history") is not None:
             held = int(rules["history_len"][s])

@@ -281,6 +281,25 @@ def test_padding_invalid_lanes_and_bits():
     call.check()
 
 
+def test_the_largest_temperature_tells_far_logits_apart():
+    call = Call(2, 3, 300, FP, FP, bias=0, history=0, tokens=False, seed=15)
+    call.logits *= 2.0 ** 124
+    call.rules["temperature"][:] = 3.4e38
+    call.check()
+
+
+@pytest.mark.parametrize("rep", [2.0 ** -126, 2.0 ** -127, 1e-45, 2.0 ** 126, 1.5 * 2.0 ** 126, 2.0 ** 127])
+def test_repetitions_at_the_ends(rep):
+    """A factor whose reciprocal is no normal number is refused; at the ends of the others no finite result is lost (logits
+    of 2^-20 .. 2^-10, so that a quotient by 2^-126 is finite, one by 2^126 loses at most 2^-150)."""
+    call = Call(2, 3, 200, FP, FP, bias=0, temp=False, seed=14, mask=False)
+    call.logits = call.logits.sign() * 2.0 ** call.logits.abs().clamp(0, 10).neg().sub(10)
+    for name in ("presence", "frequency"):
+        call.rules[name][:] = 0
+    call.rules["repetition"][:] = rep
+    call.check(expect=0 if 2.0 ** -126 <= rep <= 2.0 ** 126 else L.RULE)
+
+
 def test_rows_of_a_padded_vocabulary_and_shared_slots():
     call = Call(3, 4, 501, seed=11)
     wide = torch.full((3, 4, 520), 1e9, dtype=BF, device="cuda")
