@@ -6,6 +6,12 @@
 namespace gdn {
 namespace {
 
+// Workgroups of the kernel for few rows a CU.  Float32 rows of 256 values: one, whose waves use 414 registers; within the 256
+// of two, 95 of them go through memory (ragged lanes, D = 256, with two and with one: 32 of decode up to 8192 tokens 639 us
+// and 308, five of eight nodes up to 2999 97 and 51, one of decode at 1000 20.5 and 15.7).  Narrower ones keep two, with 15
+// to 25 registers in memory (the 32 lanes at D = 128 106 us and 133, at D = 64 55 and 69).
+constexpr int few_blocks(int row_bytes) { return row_bytes == 1024 ? 1 : 2; }
+
 template <typename T, int D, int BM>
 __global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) void attn_rows_kv4_kernel(AttnArgs a, AttnPlan plan) {
     attn_rows<T, D, BM, true>(a, plan);
@@ -15,7 +21,7 @@ __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kv4_kernel(AttnArgs
     attn_pair<T, true>(a, plan);
 }
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kv4_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * kFewWaves, few_blocks(D * sizeof(T))) void attn_few_kv4_kernel(AttnArgs a, AttnPlan plan) {
     attn_few<T, D, true>(a, plan);
 }
 template <typename T, int D>
@@ -79,7 +85,8 @@ AttnPlan attn_plan_kv4(const AttnDims &d) {
         return p;
     }
     AttnPlan p{kFewRows, 1, 1};
-    const int64_t least = few_tile(row_bytes, true) * kFewWaves, most = std::min<int64_t>((held + least - 1) / least, 64), round = 512;
+    const int64_t least = few_tile(row_bytes, true) * kFewWaves, most = std::min<int64_t>((held + least - 1) / least, 64);
+    const int64_t round = 256 * few_blocks(row_bytes);  // of workgroups
     p.splits = (int)std::min<int64_t>(most, groups < round ? round / groups : 1);
     return p;
 }

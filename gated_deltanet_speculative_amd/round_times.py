@@ -1,6 +1,7 @@
-"""Times of the gdn_round.h calls over the cases of perf/operators.py, beside their floors.
+"""Times of the gdn_round.h calls over the cases of perf/operators.py, beside their floors; with --more of the gdn_kv4.h and
+gdn_logits.h calls over those of perf/more_operators.py.
 
-    python -m gated_deltanet_speculative_amd.round_times [--only TEXT] [--further] [--draw N --seed S] [--plain] [--errors]
+    python -m gated_deltanet_speculative_amd.round_times [--more] [--only TEXT] [--further] [--draw N --seed S] [--plain] [--errors]
 
 Prints per case the microseconds of one pass among others (calls through the Python binding one after the other,
 over three sets of inputs in turn; the median of five loops) and the floor: the larger of bytes / the rate of a large
@@ -13,7 +14,7 @@ the file does not list, --draw N cases drawn from its ranges with the given seed
 
 The first runs each case without timing it, for a profiler (with --pmc FETCH_SIZE and --pmc WRITE_SIZE for the counters);
 the second prints each case's kernels from the CSV files: median duration, read and written MB as the counters report
-them.  Both take --only, --further, --draw and --seed, which have to be the same.
+them.  Both take --more, --only, --further, --draw and --seed, which have to be the same.
 """
 
 from __future__ import annotations
@@ -57,11 +58,23 @@ FURTHER = [
     # wide heads' commit
     dict(name="commit 4x16 l16 wide", op="commit", C=4, N=16, Hkv=2, D=256, layers=16, ctx=500, page=64, dtype="bf16", tree=True),
 ]
+# over a 4-bit cache
+FURTHER_MORE = [
+    dict(_WIDE, name="attn decode 64x8k wide", C=64, N=1, Hq=16, Hkv=2, ctx=8192, tree=False, ragged=True),
+    dict(_WIDE, name="attn tree 4x16 8k wide", C=4, N=16, Hq=24, Hkv=4, ctx=8192, tree=True, ragged=False),
+    dict(name="attn tree 1x16 8k", op="attn", C=1, N=16, Hq=32, Hkv=8, D=128, ctx=8192, page=64, dtype="bf16", tree=True,
+         ragged=False, gate=False),
+    dict(name="attn tree 4x16 1k", op="attn", C=4, N=16, Hq=32, Hkv=8, D=128, ctx=1000, page=64, dtype="bf16", tree=True,
+         ragged=False, gate=False),
+    dict(name="attn chain 5x8 f32 256", op="attn", C=5, N=8, Hq=8, Hkv=8, D=256, ctx=2999, page=48, dtype="f32", tree=False,
+         ragged=True, gate=False),
+]
 
 
-def operators():
+def operators(more=False):
     """The cases' file, as a module."""
-    spec = importlib.util.spec_from_file_location("round_operators", os.path.join(ROOT, "perf", "operators.py"))
+    name = "more_operators.py" if more else "operators.py"
+    spec = importlib.util.spec_from_file_location("round_operators", os.path.join(ROOT, "perf", name))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     return m
@@ -70,7 +83,8 @@ def operators():
 def cases(ops, further=False, draws=0, seed=0, only=""):
     rng = random.Random(seed)
     drawn = [dict(ops.draw(rng), name=f"draw {k}") for k in range(draws)]
-    return [c for c in (*ops.listed(), *(FURTHER if further else ()), *drawn) if only in c["name"]]
+    beside = FURTHER if ops.__file__.endswith(os.sep + "operators.py") else FURTHER_MORE
+    return [c for c in (*ops.listed(), *(beside if further else ()), *drawn) if only in c["name"]]
 
 
 def prepare(ops, case, seed):
@@ -169,6 +183,7 @@ def summary(names, trace, fetch=None, write=None):
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--more", action="store_true", help="the cases of perf/more_operators.py")
     ap.add_argument("--only", default="", help="cases whose name holds this text")
     ap.add_argument("--further", action="store_true")
     ap.add_argument("--draw", type=int, default=0)
@@ -178,7 +193,7 @@ def main(argv=None):
     ap.add_argument("--passes", type=int, default=0, help="passes of each case, one loop, without rates (for a profiler)")
     ap.add_argument("--summary", nargs="+", metavar="CSV")
     a = ap.parse_args(argv)
-    ops = operators()
+    ops = operators(a.more)
     if a.summary:
         print(summary([c["name"] for c in cases(ops, a.further, a.draw, a.seed, a.only)], *a.summary))
         return
