@@ -11,6 +11,12 @@
 // a row, the second joins them and computes each value again (reading a logit twice costs less than writing
 // it in 32 bits and reading that).  Bound by bytes where there are many rows, by the chain slot, history,
 // LDS, logits and by launches where there are few.
+//
+// 4 lanes of 16 nodes, 130001 tokens, every rule, bfloat16 to float32 probabilities: 16.6 + 17.4 us for 17 and 17 + 33 MB (about half
+// of it the vector work, some 25 operations a value, the rest loads that one row ahead does not cover); one node of 4 lanes,
+// 32768 tokens, bfloat16 logits: 5.3 us.  Eight tokens a thread and 512 threads: with 16 and 256 the constants of a thread's tokens
+// go through memory (54.6 us for both launches); two rows copied out in the loop use 162 registers, and fewer workgroups fit
+// (36).
 #include "logits_internal.h"
 #include "round_device.h"
 
@@ -168,9 +174,12 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
     if (a.tokens) tok = a.tokens[node];
     Parts parts;
     if constexpr (MODE == kProbabilities) parts.load(Parts::of(a, c, min(i0 + wave, a.N - 1)), 0);
+    // (a row's words of the mask stay as they are until the row's turn: to take a bit out of one is to wait for every load)
     const int mask_words = (a.V + 31) / 32;
     tv raw[GR];
     unsigned allow[GR];
+#pragma unroll
+    for (int g = 0; g < GR; ++g) allow[g] = ~0u;
     auto load = [&](int i) {
         const int64_t row = (int64_t)c * a.N + i;
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
@@ -183,9 +192,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) raw[g][e] = x + e < a.V ? p[x + e] : (T)0.f;
             }
-            allow[g] = (1u << VEC) - 1u;
-            if (a.mask && x < a.V) allow[g] = (unsigned)a.mask[row * mask_words + x / 32] >> (x & 31);
-            if (x + VEC > a.V) allow[g] &= x < a.V ? (1u << (a.V - x)) - 1u : 0u;
+            if (a.mask) allow[g] = (unsigned)a.mask[row * mask_words + min(x, a.V - 1) / 32];
         }
     };
     load(i0);
@@ -312,14 +319,12 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
         }
         lds_barrier();
     }
-    // ---- this thread's tokens: group g from x0 + (g kThreads + tid) VEC on.  With r >= 1, v > 0 ? v / r : v r is the smaller
-    // of v / r and v r (with r < 1 the larger), so a logit l becomes the smaller of l up + cu and l down + cd, whose
-    // constants hold the biases and what the occurrences take off.  `on`: the nodes with this token.
+    // ---- this thread's tokens: group g from x0 + (g kThreads + tid) VEC on.  A logit l becomes (l + b) up - less above zero and
+    // (l + b) down - less elsewhere.  `on`: the nodes with this token.
     auto token_of = [&](int q) { return (q / VEC * kThreads + tid) * VEC + q % VEC; };
-    float b[W], up[W], down[W], cu[W], cd[W];
+    float b[W], up[W], down[W], less[W];
     unsigned w[W], on[W], drafts = 0;
     const float inv = 1.f / rep, k2 = per_temperature(temp);
-    const bool shrinks = rep >= 1.f;
 #pragma unroll
     for (int q = 0; q < W; ++q) {
         w[q] = s_word[token_of(q)];
@@ -327,9 +332,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
         const bool seen = (w[q] & (kCount | kPrompt)) != 0;
         up[q] = seen ? inv : 1.f;
         down[q] = seen ? rep : 1.f;
-        const float less = w[q] & kCount ? fmaf(freq, (float)(w[q] & kCount), pres) : 0.f;
-        cu[q] = fmaf(b[q], up[q], -less);
-        cd[q] = fmaf(b[q], down[q], -less);
+        less[q] = w[q] & kCount ? fmaf(freq, (float)(w[q] & kCount), pres) : 0.f;
         on[q] = 0;
         drafts |= w[q];
     }
@@ -344,22 +347,20 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
             for (int q = 0; q < W; ++q) on[q] |= t == q / VEC * kThreads * VEC + lane * VEC + q % VEC ? 1u << j : 0u;
         }
     }
+    unsigned edge[GR];  // the group's tokens inside the vocabulary
+#pragma unroll
+    for (int g = 0; g < GR; ++g) {
+        const int held_back = min(max(x0 + (g * kThreads + tid + 1) * VEC - a.V, 0), VEC);
+        edge[g] = ((1u << VEC) - 1u) >> held_back;
+    }
     const bool cut = a.mask || x0 + kChunk > a.V;  // some token of the stretch may not be allowed
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         float z[W];
-        if (shrinks) {
 #pragma unroll
-            for (int q = 0; q < W; ++q) {
-                const float l = (float)raw[q / VEC][q % VEC];
-                z[q] = fminf(fmaf(l, up[q], cu[q]), fmaf(l, down[q], cd[q]));
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < W; ++q) {
-                const float l = (float)raw[q / VEC][q % VEC];
-                z[q] = fmaxf(fmaf(l, up[q], cu[q]), fmaf(l, down[q], cd[q]));
-            }
+        for (int q = 0; q < W; ++q) {
+            const float v = (float)raw[q / VEC][q % VEC] + b[q];
+            z[q] = fmaf(v, v > 0.f ? up[q] : down[q], -less[q]);
         }
         if (drafted) {
             const unsigned path = s_anc[i];
@@ -372,9 +373,16 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
         }
         if (cut)
 #pragma unroll
-            for (int q = 0; q < W; ++q) {  // (bit by bit: all ones where the token is allowed)
-                const int keep = (int)(allow[q / VEC] << (31 - q % VEC)) >> 31;
-                z[q] = __int_as_float((keep & __float_as_int(z[q])) | (~keep & __float_as_int(kNegInf)));
+            for (int g = 0; g < GR; ++g) {  // (bit by bit: all ones where the token is allowed; opaque, or it becomes compares and selects)
+                const int x = x0 + (g * kThreads + tid) * VEC;
+                const unsigned bits = (allow[g] >> (x & 31)) & edge[g];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    int keep = (int)(bits << (31 - e)) >> 31;
+                    asm("" : "+v"(keep));
+                    float &zz = z[g * VEC + e];
+                    zz = __int_as_float((keep & __float_as_int(zz)) | (~keep & __float_as_int(kNegInf)));
+                }
             }
         if (i + 1 < i1) load(i + 1);
         if constexpr (MODE == kStats) {

@@ -1,8 +1,11 @@
 // Rows of 4-bit caches as values, for gfx950: every layer's rows first .. first + N_c - 1 of the lanes' slots.
 //
-// Bound by bytes: 0.53 of a value read and 2 or 4 bytes of it written.  A lane carries 8 values (a word of codes): D / 8
-// lanes a row, consecutive (row, head) pairs of one layer, K and V in consecutive lanes' order of the output, so
-// that stores are whole lines.  A workgroup finds its tokens' pages first, one thread a token.
+// Bound by bytes: 0.53 bytes of a value read and 2 or 4 written.  A lane carries 8 values (a word of codes): D / 8 lanes
+// a row, consecutive (row, head) pairs in the output's order, so that stores are whole lines.  A workgroup takes
+// either K or V, and finds its tokens' pages first, one thread a token; four rows of a thread are in flight.
+//
+// 4095 rows of 16 layers, 8 heads of 128, float16: 70 us, 4.9 TB/s (K and V in one workgroup, one row of a thread at a time: 76);
+// 64 lanes of 32 rows of 16 layers, 8 heads of 128: 42.7 us, 4.0 TB/s (46.6); 64 rows of a layer: 4.2 us (6.8).
 #include "round_device.h"
 
 namespace gdn {

@@ -1,6 +1,11 @@
 // Attention over the paged cache of 4-bit values, for gfx950: the kernels of paged_attention.h with rows that become
 // values of the queries' type on their way into LDS (many query rows) or into an operand (few), how a call is divided
 // over them, and their launches.
+//
+// What bounds them: many query rows the products and the softmax, as over 16 bits (two chunks of 2048 behind 16k, D = 256,
+// bfloat16: 1263 us, 723 TFLOP/s, and 1269 over a 16-bit cache); 17 to 64 rows the tiles' chain of load, conversion, LDS
+// and products, with two waves a SIMD to cover it (trees of 4 x 16 nodes behind 8192, 32 / 8 heads of 128: 25 us for 19 MB
+// and 8.6 GFLOP, and 5.4 for the join; over 16 bits 34); few rows the bytes.
 #include "paged_attention.h"
 
 namespace gdn {
