@@ -12,11 +12,11 @@
 // it in 32 bits and reading that).  Bound by bytes where there are many rows, by the chain slot, history,
 // LDS, logits and by launches where there are few.
 //
-// 4 lanes of 16 nodes, 130001 tokens, every rule, bfloat16 to float32 probabilities: 16.6 + 17.4 us for 17 and 17 + 33 MB (about half
-// of it the vector work, some 25 operations a value, the rest loads that one row ahead does not cover); one node of 4 lanes,
-// 32768 tokens, bfloat16 logits: 5.3 us.  Eight tokens a thread and 512 threads: with 16 and 256 the constants of a thread's tokens
-// go through memory (54.6 us for both launches); two rows copied out in the loop use 162 registers, and fewer workgroups fit
-// (36).
+// 4 lanes of 16 nodes, 130001 tokens, every rule, bfloat16 to float32 probabilities: 15.5 + 16.0 us for 17 and 17 + 33 MB (some
+// 5 us of each until the first row is worked on, then about 15 operations and an exponential a value); 32 lanes of 32:
+// 352 us, 3.0 TB/s over both launches; one node of 4 lanes, 32768 tokens, bfloat16 logits: 5.3 us.  Eight tokens a thread and
+// 512 threads: with 16 and 256 the constants of a thread's tokens went through memory (54.6 us and 44).  Two rows in flight
+// instead of one: 30.7 us and 30.3, 32 lanes of 32 369 and 352.
 #include "logits_internal.h"
 #include "round_device.h"
 

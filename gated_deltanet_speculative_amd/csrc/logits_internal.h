@@ -21,7 +21,7 @@ struct LogitArgs {
 constexpr int kLogitThreads = 512, kLogitTokens = 8, kLogitChunk = kLogitThreads * kLogitTokens;  // a stretch of the vocabulary
 inline int logit_chunks(int V) { return (V + kLogitChunk - 1) / kLogitChunk; }
 // Nodes of a workgroup: all of a lane's, fewer where there would be less than 512 workgroups, two a CU (4 lanes of 16 nodes,
-// 130001 tokens, probabilities: 31 us, with 256 workgroups 34.8)
+// 130001 tokens, probabilities: with 512 workgroups 31 us, with 256 34.8)
 inline int logit_rows(int C, int N, int V) {
     const int64_t groups = (int64_t)C * logit_chunks(V), parts = (511 + groups) / groups;
     return parts >= N ? 1 : (int)((N + parts - 1) / parts);
