@@ -397,7 +397,7 @@ struct FourTile {
 constexpr int group_blocks(int value_bytes, int rows) { return value_bytes == 4 && rows == 64 ? 1 : 2; }  // waves a SIMD, at least
 
 template <typename T, int D, int BM, bool kFour>
-__device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &plan) {
+__device__ __forceinline__ void attn_rows(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = group_waves(BM), kThreads = 64 * kWaves, RT = group_tiles(BM), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
     static_assert(BM == 16 * RT * kWaves && RPP <= TOK, "");
@@ -774,7 +774,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs &a, const AttnPlan &pla
 constexpr int kPairRows = 128, kPairThreads = 512;
 
 template <typename T, bool kFour>
-__device__ __forceinline__ void attn_pair(const AttnArgs &a, const AttnPlan &plan) {
+__device__ __forceinline__ void attn_pair(AttnArgs a, AttnPlan plan) {
     constexpr int D = 256, RB = 512, TOK = 64, RT = 2, NT = 2, NS = RB / 64, ND = 8;  // NT, ND: of this wave's half
     constexpr int BM = kPairRows, TPR = RB / 16, RPP = kPairThreads / TPR, NP = TOK / RPP;
     static_assert(sizeof(T) == 2, "");
@@ -1129,7 +1129,7 @@ constexpr int kFewWaves = 4, kFewRows = 16;
 constexpr int few_tile(int row_bytes, bool four) { return four ? (row_bytes < 256 ? 64 : 16384 / row_bytes) : 8192 / row_bytes; }
 
 template <typename T, int D, bool kFour>
-__device__ __forceinline__ void attn_few(const AttnArgs &a, const AttnPlan &plan) {
+__device__ __forceinline__ void attn_few(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = few_tile(RB, kFour), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kFour ? 64 / (D / 32) : 64 / TPR, NP = TOK / RPP;
     constexpr bool kPairs = sizeof(T) == 2 && TOK >= 32;  // the second product in steps of 32 rows
@@ -1433,7 +1433,7 @@ constexpr int kJoinWaves = 4;
 // Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.  What there is to
 // join stands beside the parts (join_pairs), so that no read waits for another but the first.
 template <typename T, int D>
-__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnPlan &plan) {
+__device__ __forceinline__ void attn_join(AttnArgs a, AttnPlan plan) {
     constexpr int W = D / 64, kAhead = 8;  // parts loaded together
     typedef float vw __attribute__((ext_vector_type(W)));
     typedef T tw __attribute__((ext_vector_type(W)));
