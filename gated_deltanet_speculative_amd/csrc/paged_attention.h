@@ -1122,7 +1122,7 @@ __device__ __forceinline__ void attn_pair(AttnArgs a, AttnPlan plan) {
 // 510 us); one lane behind 1003 tokens: 7 us, and 3.2 us for the join.
 //
 // A 4-bit cache has a fourth of the bytes for as many rows: a tile is 16 KiB of V as values (at most 64 rows), so that
-// a wave has 2 to 4 KiB of K and of V in flight.  The same 64 lanes over it, 864 MB: 178 us, 4.85 TB/s, 95% of a copy (lanes of
+// a wave has 2 to 4 KiB of K and of V in flight.  The same 64 lanes over it, 864 MB: 178 us, 4.85 TB/s, 94% of a copy (lanes of
 // equal length 158 us, 5.45 TB/s: the last workgroups of a ragged batch run alone); one lane behind 1003 tokens: 7.6 us.  Tiles
 // of 8 KiB in three workgroups a CU: 175 us; two tiles in flight: 177.
 constexpr int kFewWaves = 4, kFewRows = 16;
