@@ -71,15 +71,25 @@ __device__ inline float wave_sum(float x) {
     return (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
 }
 constexpr int kAhead = 4;  // loads of a thread that are requested together
+// A temperature that is no normal number: its factor would pass the largest number, and halves of differences of its size lose
+// their last bit.
+__device__ inline bool steep(float temp) { return temp > 0.f && temp < 0x1p-126f; }
 // 2 log2(e) / T, finite for T = 0; never 0 (2^-127 for the largest T: not a normal number, but exact to 2^-22), so that
-// -infinity times it is -infinity.  It multiplies half of z - m, which no two finite numbers carry out of range.
-__device__ inline float per_temperature(float temp) { return fminf(2.8853900817779268f / temp, 3.4e38f); }
-__device__ inline float half_below(float z, float half_m) { return fmaf(z, 0.5f, -half_m); }
-// e^{(z - m) / T} with k = 2 log2(e) / T; 1 at the maximum even where that is infinite, 0 for -infinity
-__device__ inline float weight(float z, float m, float k) {
-    const float top = m == kNegInf ? 0.f : m;
-    return __builtin_amdgcn_exp2f(z == top ? 0.f : half_below(z, 0.5f * top) * k);
+// -infinity times it is -infinity.  It multiplies half of z - m, which no two finite numbers carry out of range; for a steep
+// T, log2(e) / (2^64 T), of 2^64 (z - m): out of range only where the weight is 0.
+__device__ inline float per_temperature(float temp) {
+    return steep(temp) ? 1.4426950408889634f / (temp * 0x1p64f) : fminf(2.8853900817779268f / temp, 3.4e38f);
 }
+__device__ inline float half_below(float z, float half_m) { return fmaf(z, 0.5f, -half_m); }
+// e^{(z - m) / T}; 1 at the maximum even where that is infinite, 0 for -infinity
+struct Weight {
+    float k;  // per_temperature(temp)
+    bool is_steep;
+    __device__ float operator()(float z, float m) const {
+        const float top = m == kNegInf ? 0.f : m;
+        return __builtin_amdgcn_exp2f(z == top ? 0.f : (is_steep ? (z - top) * 0x1p64f : half_below(z, 0.5f * top)) * k);
+    }
+};
 
 // Entries of a slot's history from k0 on, four at a time: entry 4 (j kThreads + tid) + k0 and the next three, or, where
 // these would pass the end, the last four (of which `from` leaves out what another thread has; fewer than four in all:
@@ -130,7 +140,7 @@ struct Parts {
 };
 __device__ inline Total row_total(const LogitArgs &a, int c, int i, float temp, Parts &p) {  // p: the first ones, loaded
     const int parts = gridDim.x * kWaves;
-    const float k2 = per_temperature(temp);
+    const Weight weight{per_temperature(temp), steep(temp)};
     const v4f *row = Parts::of(a, c, i);
     Best b{kNegInf, 0x7fffffff};
     float sum = 0.f;
@@ -140,14 +150,14 @@ __device__ inline Total row_total(const LogitArgs &a, int c, int i, float temp, 
         Best to = b;
 #pragma unroll
         for (int j = 0; j < kParts; ++j) to = better(to, Best{p.v[j][0], __float_as_int(p.v[j][2])});
-        if (k0) sum = sum == 0.f ? 0.f : sum * weight(b.v, to.v, k2);  // (a part of nothing has sum 0; NaN sums stay NaN)
+        if (k0) sum = sum == 0.f ? 0.f : sum * weight(b.v, to.v);  // (a part of nothing has sum 0; NaN sums stay NaN)
 #pragma unroll
-        for (int j = 0; j < kParts; ++j) sum += p.v[j][1] == 0.f ? 0.f : p.v[j][1] * weight(p.v[j][0], to.v, k2);
+        for (int j = 0; j < kParts; ++j) sum += p.v[j][1] == 0.f ? 0.f : p.v[j][1] * weight(p.v[j][0], to.v);
         b = to;
     }
     Best all{wave_max(b.v), 0x7fffffff};
     if (temp == 0.f) all = wave_best(b);
-    return Total{all.v, wave_sum(sum == 0.f ? 0.f : sum * weight(b.v, all.v, k2)), all.x};
+    return Total{all.v, wave_sum(sum == 0.f ? 0.f : sum * weight(b.v, all.v)), all.x};
 }
 
 template <typename T, typename O, int MODE>
@@ -325,6 +335,7 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
     float b[W], up[W], down[W], less[W];
     unsigned w[W], on[W], drafts = 0;
     const float inv = 1.f / rep, k2 = per_temperature(temp);
+    const Weight weight{k2, steep(temp)};
 #pragma unroll
     for (int q = 0; q < W; ++q) {
         w[q] = s_word[token_of(q)];
@@ -398,12 +409,12 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
                 top = wave_best(top);
             }
             float sum = 0.f;
-            if (fabsf(top.v) < __builtin_inff()) {
+            if (fabsf(top.v) < __builtin_inff() && !steep(temp)) {
 #pragma unroll
                 for (int q = 0; q < W; ++q) sum += __builtin_amdgcn_exp2f(half_below(z[q], 0.5f * top.v) * k2);
             } else {
 #pragma unroll
-                for (int q = 0; q < W; ++q) sum += weight(z[q], top.v, k2);
+                for (int q = 0; q < W; ++q) sum += weight(z[q], top.v);
             }
             sum = wave_sum(sum);
             if (lane == 0)
@@ -413,14 +424,14 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
             if constexpr (MODE == kProbabilities) {
                 const Total t = s_total[i - i0];
                 const float scale = t.sum == 0.f ? 0.f : 1.f / t.sum;
-                if (temp > 0.f && fabsf(t.top) < __builtin_inff()) {
+                if (temp >= 0x1p-126f && fabsf(t.top) < __builtin_inff()) {
 #pragma unroll
                     for (int q = 0; q < W; ++q) z[q] = __builtin_amdgcn_exp2f(half_below(z[q], 0.5f * t.top) * k2) * scale;
                 } else {
                     const int best = t.top == kNegInf ? -1 : t.at;
 #pragma unroll
                     for (int q = 0; q < W; ++q)
-                        z[q] = temp > 0.f ? weight(z[q], t.top, k2) * scale : x0 + token_of(q) == best ? 1.f : 0.f;
+                        z[q] = temp > 0.f ? weight(z[q], t.top) * scale : x0 + token_of(q) == best ? 1.f : 0.f;
                 }
             }
             O *out = static_cast<O *>(a.out) + ((int64_t)c * a.N + i) * a.V;
