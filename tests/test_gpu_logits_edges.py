@@ -1,12 +1,15 @@
-"""Edges of the logits' rules on the GPU against the fp64 oracle: temperatures that are no normal numbers."""
+"""Edges of the logits' rules on the GPU against the fp64 oracle: temperatures that are no normal numbers; long
+lists of biases with tokens that occur twice."""
 
 import numpy as np
 import pytest
+import torch
 
+import gated_deltanet_speculative_amd as gdn
 from gpu_util import log
 from oracle import logits_oracle as L
 from round_util import as_numpy, dev
-from test_gpu_logits import FP, Call
+from test_gpu_logits import BF, FP, Call
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +43,73 @@ def test_temperatures_below_the_normal_numbers(temp, V):
             worst = max(worst, float((np.abs(g[c, i] - want) / tol).max()))
     log(f"[logits] T={temp:.1e} V={V}: worst error {worst:.3f} of the tolerance")
     assert worst <= 1 and g[0, 2, 5] == 1
+
+
+@pytest.mark.parametrize("kind", ["one", "pairs", "equal", "zeros"])
+@pytest.mark.parametrize("B", [3, 513, 1024])
+@pytest.mark.parametrize("temp", [False, True])
+def test_long_bias_lists_with_tokens_that_occur_twice(B, kind, temp):
+    """The sums bit for bit: float32 additions in the list's order (no other rule, so out is their sum with the logit); with a
+    temperature the same probabilities as the summed list gives."""
+    V, P = 9001, 3
+    rng = np.random.default_rng(B)
+    toks = np.stack([rng.permutation(V)[:B] for _ in range(P)]).astype(np.int32)
+    if kind == "one":
+        toks[:, -1] = toks[:, 0]
+    elif kind == "pairs":  # spread over the stretches, some three times, with ids outside the vocabulary between them
+        toks[:, 2::3], toks[:, B // 2] = toks[:, :len(toks[0, 2::3])], -1
+        toks[1, ::5] = 2 ** 31 - 1
+    else:
+        toks[:] = V - 1
+    vals = (rng.standard_normal((P, B)) * 10.0 ** rng.integers(-3, 4, (P, B))).astype(np.float32)
+    if kind == "zeros":
+        vals[:] = -0.0
+    call = Call(2, 3, V, FP, FP, history=0, bias=B, mask=False, tokens=False, temp=temp, extra=1, seed=3)
+    temperature = call.rules.get("temperature")
+    call.rules = dict(P=P, bias_tokens=toks, bias=vals)
+    summed = np.full((P, V), -0.0, np.float32)
+    for s in range(P):
+        for t, v in zip(toks[s], vals[s]):
+            if 0 <= t < V:
+                summed[s, t] += v
+    if temp:
+        call.rules["temperature"] = temperature
+        got, status = call.run()
+        call.rules = dict(P=P, temperature=temperature)
+        call.sh = call.sh._replace(max_bias=0)
+        call.logits = call.logits + dev(summed[call.slots])[:, None]
+        assert status == 0 and torch.equal(got.view(torch.int32), call.run()[0].view(torch.int32))
+        return
+    got, status = call.run()
+    assert status == 0
+    want = as_numpy(call.logits) + summed[call.slots][:, None]
+    assert np.array_equal(as_numpy(got).view(np.int32), want.view(np.int32))
+
+
+def test_a_token_twice_costs_little():
+    """A list of 1024 biases with one token twice, and of one token throughout, beside one without (scans of the list in memory took
+    47 times the whole call for either).  One token: a wave looks at 16 entries a lane.  All the same: 1024 additions in
+    the list's order, each behind 8 dependent scalar and lane instructions of some 10 cycles, 1024 * 80 / 2.4 GHz = 34 us
+    beside a call of 4 to 5 us."""
+    C, V, B = 4, 32768, 1024
+    call = Call(C, 1, V, BF, BF, history=0, bias=B, mask=False, tokens=False, tree=False, temp=False, extra=0, seed=4)
+    out, slots, status = torch.empty(C, 1, V, dtype=BF, device="cuda"), dev(call.slots), torch.zeros(1, dtype=torch.int32, device="cuda")
+    us = {}
+    for kind in ("none", "one", "equal"):
+        toks = np.stack([call.rng.permutation(V)[:B] for _ in range(C)]).astype(np.int32)
+        if kind == "one":
+            toks[:, -1] = toks[:, 0]
+        if kind == "equal":
+            toks[:] = 9
+        toks, vals, times = dev(toks), dev(call.rules["bias"]), []
+        for _ in range(7):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(50):
+                gdn.adjust_logits(call.sh, call.logits, slots, bias_tokens=toks, bias=vals, out=out, status=status)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 20)
+        us[kind] = min(times)
+    log(f"[logits] 1024 biases: {us} us")
+    assert us["one"] < 3 * us["none"] and us["equal"] < 16 * us["none"]
