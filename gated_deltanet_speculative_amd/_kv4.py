@@ -125,6 +125,14 @@ def kv4_commit_layers(sh: R.AttnShape, caches, slot_ids, page_table, seq_len, ac
     return new_len
 
 
+def _layers(caches) -> int:
+    """The layers of a Kv4Cache with a leading layer axis, or of a sequence of one a layer; 1 for what the call refuses."""
+    if isinstance(caches, tuple) and len(caches) == 4 and not isinstance(caches[0], tuple):
+        k = caches[0]
+        return k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 5 else 1
+    return len(caches) if hasattr(caches, "__len__") else 1
+
+
 def kv4_read_layers(sh: R.AttnShape, caches, slot_ids, page_table, first_row, lane_nodes=None, k_out=None, v_out=None,
                     status=None):
     """Rows first_row[c] .. first_row[c] + N - 1 of every lane's slot as values of sh.dtype, for every layer (caches as in
@@ -134,8 +142,7 @@ def kv4_read_layers(sh: R.AttnShape, caches, slot_ids, page_table, first_row, la
     call, f = _call_of("kv4_read_layers")
     held, shape = _shape(sh)  # (held: the struct lives through the call)
     if k_out is None or v_out is None:
-        n = caches.k.shape[0] if isinstance(caches, Kv4Cache) else len(caches)
-        rows = (n, sh.n_seqs, sh.n_nodes, sh.n_kv_heads, sh.head_dim)
+        rows = (_layers(caches), sh.n_seqs, sh.n_nodes, sh.n_kv_heads, sh.head_dim)
         k_out, v_out = (torch.zeros(rows, dtype=sh.dtype, device=device) if t is None else t for t in (k_out, v_out))
     status = R._status_word(status, device)
     R._call(device, call, "gdn_kv4_read_layers", f, shape, device, caches, slot_ids, page_table, first_row,

@@ -106,6 +106,13 @@ PyObject *view(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A dimension of a tensor argument, -1 where it is none
+int64_t size_of(PyObject *o, int64_t dims, int64_t k) {
+    if (!THPVariable_Check(o)) return -1;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    return t.dim() == dims ? t.size(k) : -1;
+}
+
 // The arguments of one call, taken in their order.  After the first unsuitable one `bad` is set, with the Python error, and
 // every further one is NULL.
 class Arguments {
@@ -191,9 +198,8 @@ public:
     int caches(const gdn_attn_shape &s, gdn_kv4_cache (&to)[GDN_MAX_LAYERS]) {
         PyObject *o = bad ? nullptr : next();
         if (!o) return 0;
-        if (PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4 && THPVariable_Check(PyTuple_GET_ITEM(o, 0))) {
-            const at::Tensor &k = THPVariable_Unpack(PyTuple_GET_ITEM(o, 0));
-            const int64_t n = k.dim() == 5 ? k.size(0) : 0;
+        if (PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4 && !PyTuple_Check(PyTuple_GET_ITEM(o, 0))) {
+            const int64_t size = size_of(PyTuple_GET_ITEM(o, 0), 5, 0), n = size < 0 ? 1 : size;  // (no such tensor: refused below)
             if (!count(n)) return 0;
             const gdn_kv4_cache first = four(o, s, n);
             const size_t rows = (size_t)s.n_pages * s.n_kv_heads * s.page_size, codes = rows * (s.head_dim / 2), scales = rows * (s.head_dim / 32);
@@ -283,13 +289,6 @@ public:
 };
 
 at::ScalarType type_of(int32_t dtype) { return dtype == GDN_DTYPE_F32 ? at::kFloat : dtype == GDN_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
-
-// A dimension of a tensor argument, -1 where it is none
-int64_t size_of(PyObject *o, int64_t dims, int64_t k) {
-    if (!THPVariable_Check(o)) return -1;
-    const at::Tensor &t = THPVariable_Unpack(o);
-    return t.dim() == dims ? t.size(k) : -1;
-}
 
 PyObject *rope_kv4_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
