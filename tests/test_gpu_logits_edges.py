@@ -1,5 +1,5 @@
 """Edges of the logits' rules on the GPU against the fp64 oracle: temperatures that are no normal numbers; long
-lists of biases with tokens that occur twice."""
+lists of biases with tokens that occur twice; every value of rows with infinities, NaN and the type's lowest value."""
 
 import numpy as np
 import pytest
@@ -9,7 +9,7 @@ import gated_deltanet_speculative_amd as gdn
 from gpu_util import log
 from oracle import logits_oracle as L
 from round_util import as_numpy, dev
-from test_gpu_logits import BF, FP, Call
+from test_gpu_logits import BF, FP, HF, Call, expected
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,55 @@ def test_a_token_twice_costs_little():
         us[kind] = min(times)
     log(f"[logits] 1024 biases: {us} us")
     assert us["one"] < 3 * us["none"] and us["equal"] < 16 * us["none"]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, FP), (BF, BF), (FP, FP), (HF, HF), (HF, FP)])
+@pytest.mark.parametrize("temp", [None, 1.0, 0.0])
+def test_every_value_beside_infinities_and_nan(dtype, out, temp):
+    """Row by row: infinite and masked values exactly, finite ones within `expected`.
+
+    The oracle's values are rounded to 32 bits where the type's lowest value is a row's: the call computes there (a penalty
+    beside it is lost, a repetition of it overflows), and with bfloat16's or float32's the tolerance of `expected`, which is of
+    the row's largest size, would be no test: all tokens that no rule touches have the same probability there."""
+    call = Call(1, 8, 600, dtype, out, seed=7, temp=False, bias=3)
+    s = call.slots[0]
+    call.mask[:] = -1
+    call.rules["repetition"][s], call.rules["bias_tokens"][s], call.rules["bias"][s] = 1.5, [50, 51, 52], [-np.inf, 1, 2]
+    x = call.logits
+    x[0, 0, 100] = x[0, 0, 200] = float("inf")
+    x[0, 1, :] = -float("inf")
+    x[0, 2, 77] = float("nan")
+    x[0, 3, 33], x[0, 3, 34] = float("nan"), float("inf")
+    call.mask[0, 3, 1], call.mask[0, 3, 9] = ~(3 << 1), 0x0F0F0F0F
+    x[0, 4, 5] = -float("inf")
+    call.mask[0, 4, 2:7] = 0x33333333
+    x[0, 5, :] = float("nan")
+    call.mask[0, 5] = 0
+    x[0, 6, :] = torch.finfo(dtype).min
+    call.mask[0, 7] = 0
+    x[0, 7, :] = float("inf")
+    if temp is not None:
+        call.rules["temperature"] = np.full(call.sh.n_slots, temp, np.float32)
+    got, status = call.run()
+    res, bits = call.want()
+    assert status == bits == 0
+    g, word, at = as_numpy(got).astype(np.float64), np.arange(600) // 32, np.arange(600) % 32
+    for i in range(8):
+        z, size, T = res[0, i]
+        masked = (call.mask[0, i].view(np.uint32)[word] >> at.astype(np.uint32)) & 1 == 0
+        with np.errstate(over="ignore"):
+            low = i == 6 and dtype is not HF
+            z = z.astype(np.float32).astype(np.float64) if low else z
+            want, tol = expected(z, size, T, call.sh)
+            if low and T == 1.0:
+                want = L.probabilities(z, T)
+                assert np.count_nonzero(want) > 500 and len(np.unique(want)) == 2
+                tol = want * (2.0 ** -19 + (2.0 ** -8 if out is BF else 0)) + 1e-35
+            if T is None:  # beyond the type's range: an infinity of it
+                want = np.where(np.abs(want) > float(torch.finfo(out).max) * (1 + 2.0 ** -12), np.sign(want) * np.inf, want)
+        exact = masked | ~np.isfinite(want) | ~np.isfinite(z) | (T == 0) | ((T is not None) & (want == 0))
+        assert np.array_equal(g[0, i][exact], want[exact], equal_nan=True), f"row {i}"
+        fine = ~exact
+        if fine.any():
+            ratio = np.abs(g[0, i][fine] - want[fine]) / tol[fine]
+            assert ratio.max() <= 1, f"row {i} is {ratio.max():.2f} tolerances off at {int(np.flatnonzero(fine)[np.argmax(ratio)])}"
