@@ -360,6 +360,8 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
     auto token_of = [&](int q) { return (q / VEC * kThreads + tid) * VEC + q % VEC; };
     float b[W], up[W], down[W], less[W];
     unsigned w[W], on[W], drafts = 0;
+    // (a repetition is a product with the rounded reciprocal, at most one step beside the quotient: 4 x 16 rows of 130001 29.7 us, with
+    // the product corrected to the rounded quotient 31.3, with divisions 34.0)
     const float inv = 1.f / rep, k2 = per_temperature(temp);
     const Weight weight{k2, steep(temp)};
 #pragma unroll

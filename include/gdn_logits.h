@@ -58,10 +58,12 @@ typedef struct gdn_logit_rules {
 /*
  * For every present node i of a valid lane and every token x, in float32:
  *   z = logits[c][i][x] + the sum of s's biases of x, in the list's order
- *   z = z > 0 ? z / r : z * r      where x is in s's history or on path(i)
+ *   z = z > 0 ? z * (1 / r) : z * r  where x is in s's history or on path(i)
  *   z = z - f n - p [n > 0]        n = occurrences of x in the history behind the prompt, and
  *                                  on path(i)
  *   z = -infinity                  where the mask's bit of x is 0, whatever the rest is
+ * with 1 / r rounded to float32: such a z may be one step beside z / r, and equal to another
+ * token's, or not, where that would be otherwise.
  * Without a temperature out[c][i][x] = z.  With T = temperature[s] > 0
  *   out[c][i][x] = e^{(z(x) - max z) / T} / sum_y e^{(z(y) - max z) / T}
  * (a z of +infinity counts e^0, a NaN makes its row NaN), and with T = 0 it is 1 at the

@@ -1,5 +1,6 @@
 """Edges of the logits' rules on the GPU against the fp64 oracle: temperatures that are no normal numbers; long
-lists of biases with tokens that occur twice; every value of rows with infinities, NaN and the type's lowest value."""
+lists of biases with tokens that occur twice; every value of rows with infinities, NaN and the type's lowest value; the
+rounding of a repetition."""
 
 import numpy as np
 import pytest
@@ -165,3 +166,16 @@ def test_every_value_beside_infinities_and_nan(dtype, out, temp):
         if fine.any():
             ratio = np.abs(g[0, i][fine] - want[fine]) / tol[fine]
             assert ratio.max() <= 1, f"row {i} is {ratio.max():.2f} tolerances off at {int(np.flatnonzero(fine)[np.argmax(ratio)])}"
+
+
+def test_a_repetition_is_a_product_with_the_rounded_reciprocal():
+    """As the header says, bit for bit: above zero fl(z fl(1 / r)), elsewhere fl(z r)."""
+    V, P = 4500, 4
+    call = Call(4, 1, V, FP, FP, history=V, bias=0, mask=False, tokens=False, tree=False, temp=False, extra=0, seed=5)
+    r = np.array([1.1, 1.25, 3.0, 0.7], np.float32)
+    call.rules = dict(P=P, history=np.tile(np.arange(V, dtype=np.int32), (P, 1)), history_len=np.full(P, V, np.int32),
+                      prompt_len=np.full(P, V, np.int32), repetition=r)
+    got, status = call.run()
+    x, by = as_numpy(call.logits)[:, 0], r[call.slots][:, None]
+    want = np.where(x > 0, x * (np.float32(1) / by), x * by)
+    assert status == 0 and want.dtype == np.float32 and np.array_equal(as_numpy(got)[:, 0].view(np.int32), want.view(np.int32))
