@@ -18,7 +18,7 @@
 // The cache holds values of the queries' type, or (kFour) 4-bit numbers with a power of two for every 32 values of a
 // row: those become values of the queries' type, exactly but for float16's range, on their way into LDS or into an
 // operand, and everything behind that is the same.  Internal linkage: paged_attention.hip has the kernels of the
-// first, paged_attention_kv4.hip of the second.
+// first and the join, paged_attention_kv4.hip those of the second.
 #pragma once
 
 #include <algorithm>
@@ -397,7 +397,7 @@ struct FourTile {
 constexpr int group_blocks(int value_bytes, int rows) { return value_bytes == 4 && rows == 64 ? 1 : 2; }  // waves a SIMD, at least
 
 template <typename T, int D, int BM, bool kFour>
-__device__ __forceinline__ void attn_rows(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = tile_rows(RB), kWaves = group_waves(BM), kThreads = 64 * kWaves, RT = group_tiles(BM), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kThreads / TPR, NP = TOK / RPP;  // staging: threads per row, rows a pass, passes
     static_assert(BM == 16 * RT * kWaves && RPP <= TOK, "");
@@ -773,8 +773,16 @@ __device__ __forceinline__ void attn_rows(AttnArgs a, AttnPlan plan) {
 // the weights, where K of the next tile is.
 constexpr int kPairRows = 128, kPairThreads = 512;
 
+// The text below is the kernel itself over 16 bits, and a function that the kernel calls over 4: the registers that the compiler
+// keeps in memory are others, by no rule to be seen from here (the chunks above as kernel and as function: over 16 bits 1277 us
+// and 1290, over 4 bits 1290 and 1248).
 template <typename T, bool kFour>
-__device__ __forceinline__ void attn_pair(AttnArgs a, AttnPlan plan) {
+__global__ void attn_pair_kernel(AttnArgs a, AttnPlan plan);
+#ifndef GDN_ATTN_PAIR
+#define GDN_ATTN_PAIR __global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel
+#endif
+template <typename T, bool kFour>
+GDN_ATTN_PAIR(AttnArgs a, AttnPlan plan) {
     constexpr int D = 256, RB = 512, TOK = 64, RT = 2, NT = 2, NS = RB / 64, ND = 8;  // NT, ND: of this wave's half
     constexpr int BM = kPairRows, TPR = RB / 16, RPP = kPairThreads / TPR, NP = TOK / RPP;
     static_assert(sizeof(T) == 2, "");
@@ -1128,8 +1136,14 @@ __device__ __forceinline__ void attn_pair(AttnArgs a, AttnPlan plan) {
 constexpr int kFewWaves = 4, kFewRows = 16;
 constexpr int few_tile(int row_bytes, bool four) { return four ? (row_bytes < 256 ? 64 : 16384 / row_bytes) : 8192 / row_bytes; }
 
+// Workgroups a CU.  Float32 rows of 256 4-bit values: one, whose waves use 414 registers; within the 256 of two, 95 of them go
+// through memory (ragged lanes, D = 256, with two and with one: 32 of decode up to 8192 tokens 639 us and 308, five of eight
+// nodes up to 2999 97 and 51, one of decode at 1000 20.5 and 15.7).  Narrower ones keep two, with 15 and 27 registers in
+// memory (the 32 lanes at D = 64 55 us and 69, at D = 128 106 and 133).
+constexpr int few_blocks(int row_bytes, bool four) { return four && row_bytes == 1024 ? 1 : 2; }
+
 template <typename T, int D, bool kFour>
-__device__ __forceinline__ void attn_few(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * kFewWaves, few_blocks(D * sizeof(T), kFour)) void attn_few_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int RB = D * sizeof(T), TOK = few_tile(RB, kFour), NT = TOK / 16, NS = RB / 64, ND = D / 16;
     constexpr int TPR = RB / 16, RPP = kFour ? 64 / (D / 32) : 64 / TPR, NP = TOK / RPP;
     constexpr bool kPairs = sizeof(T) == 2 && TOK >= 32;  // the second product in steps of 32 rows
@@ -1429,59 +1443,46 @@ __device__ __forceinline__ void attn_few(AttnArgs a, AttnPlan plan) {
     }
 }
 
-constexpr int kJoinWaves = 4;
-// Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.  What there is to
-// join stands beside the parts (join_pairs), so that no read waits for another but the first.
-template <typename T, int D>
-__device__ __forceinline__ void attn_join(AttnArgs a, AttnPlan plan) {
-    constexpr int W = D / 64, kAhead = 8;  // parts loaded together
-    typedef float vw __attribute__((ext_vector_type(W)));
-    typedef T tw __attribute__((ext_vector_type(W)));
-    const AttnDims &d = a.d;
-    const int lane = threadIdx.x & 63, parts = plan.splits;
-    const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
-    if (row >= all_rows) return;
-    const float *ml = join_pairs(a, plan) + row * 2, *po = a.workspace + row * D + lane * W;
-    vw v[kAhead];
-    auto load = [&](int p0) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            v[j] = *reinterpret_cast<const vw *>(po + (size_t)min(p0 + j, parts - 1) * all_rows * D);
-    };
-    load(0);
-    const float mine = ml[(size_t)min(lane, parts - 1) * all_rows * 2];
-    const float part_sum = lane < parts ? ml[(size_t)lane * all_rows * 2 + 1] : 0.f;
-    if (__builtin_amdgcn_ballot_w64(mine != mine)) return;  // an absent row
-    float mx = mine;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
-    // (a part without any attended row has weight 0; NaN sums stay NaN)
-    const float wgt = mine == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mine - mx);
-    float sum = part_sum == 0.f ? 0.f : part_sum * wgt;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
-    vw acc = 0.f;
-    for (int p0 = 0; p0 < parts; p0 += kAhead) {
-        if (p0) load(p0);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const float w = p0 + j < parts ? __shfl(wgt, p0 + j) : 0.f;
-            if (w != 0.f) acc += v[j] * w;
-        }
+// ---- the launches of one call; the join of its parts, whatever the cache holds, is launched by paged_attention.hip
+template <typename T, int D, int BM, bool kFour>
+void launch_rows(const AttnArgs &a, const AttnPlan &p, unsigned units, hipStream_t stream) {
+    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
+    hipLaunchKernelGGL((attn_rows_kernel<T, D, BM, kFour>), grid, dim3(64 * group_waves(BM)), 0, stream, a, p);
+}
+
+template <typename T, int D, bool kFour>
+hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    constexpr int RB = D * sizeof(T);
+    const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
+    if constexpr (RB < 1024 || kFour)
+        if (p.rows_per_group == kFewRows)
+            hipLaunchKernelGGL((attn_few_kernel<T, D, kFour>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
+    if constexpr (RB < 512 || sizeof(T) == 4)
+        if (p.rows_per_group == 64) launch_rows<T, D, 64, kFour>(a, p, units, stream);
+    if constexpr (RB < 512 && sizeof(T) == 2)
+        if (p.rows_per_group == 256) launch_rows<T, D, 256, kFour>(a, p, units, stream);
+    if constexpr (D == 256 && sizeof(T) == 2) {
+        if (p.rows_per_group == kPairRows)
+            hipLaunchKernelGGL((attn_pair_kernel<T, kFour>), dim3(p.tiles > 1 ? (units + 7) / 8 * 8 : units), dim3(kPairThreads), 0,
+                               stream, a, p);
+    } else if constexpr (RB < 1024) {
+        if (p.rows_per_group == 128) launch_rows<T, D, 128, kFour>(a, p, units, stream);
     }
-    const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
-    const int token = r / d.G, head = h * d.G + r - token * d.G;
-    const int64_t node = (int64_t)c * d.N + token;
-    acc = sum == 0.f ? vw(0.f) : acc / sum;
-    if (a.gate.p && sum != 0.f) {
-        const tw z = *reinterpret_cast<const tw *>(static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head + lane * W);
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] = gated(acc[i], (float)z[i], a.gate_mode);
-    }
-    tw res;
-#pragma unroll
-    for (int i = 0; i < W; ++i) res[i] = (T)acc[i];
-    *reinterpret_cast<tw *>(static_cast<T *>(a.out) + (node * d.Hq + head) * D + lane * W) = res;
+    return p.splits > 1 ? launch_attention_join(a, p, stream) : hipGetLastError();
+}
+
+template <typename T, bool kFour>
+hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    if (a.d.D == 64) return launch<T, 64, kFour>(a, p, stream);
+    if (a.d.D == 128) return launch<T, 128, kFour>(a, p, stream);
+    return launch<T, 256, kFour>(a, p, stream);
+}
+
+template <bool kFour>
+hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    if (a.d.dtype == GDN_DTYPE_BF16) return launch_t<__bf16, kFour>(a, p, stream);
+    if (a.d.dtype == GDN_DTYPE_F16) return launch_t<_Float16, kFour>(a, p, stream);
+    return launch_t<float, kFour>(a, p, stream);
 }
 
 }  // namespace

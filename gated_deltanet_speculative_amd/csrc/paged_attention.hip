@@ -5,60 +5,71 @@
 namespace gdn {
 namespace {
 
-template <typename T, int D, int BM>
-__global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) void attn_rows_kernel(AttnArgs a, AttnPlan plan) {
-    attn_rows<T, D, BM, false>(a, plan);
-}
-template <typename T>
-__global__ __launch_bounds__(kPairThreads, 2) void attn_pair_kernel(AttnArgs a, AttnPlan plan) {
-    attn_pair<T, false>(a, plan);
-}
-template <typename T, int D>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(AttnArgs a, AttnPlan plan) {
-    attn_few<T, D, false>(a, plan);
-}
+constexpr int kJoinWaves = 4;
+// Joins the parts of the cache, in their order: a wave per query row, D / 64 columns a lane.  What there is to
+// join stands beside the parts (join_pairs), so that no read waits for another but the first.
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(AttnArgs a, AttnPlan plan) {
-    attn_join<T, D>(a, plan);
-}
-
-template <typename T, int D, int BM>
-void launch_rows(const AttnArgs &a, const AttnPlan &p, unsigned units, hipStream_t stream) {
-    const dim3 grid(p.tiles > 1 ? (units + 7) / 8 * 8 : units);
-    hipLaunchKernelGGL((attn_rows_kernel<T, D, BM>), grid, dim3(64 * group_waves(BM)), 0, stream, a, p);
-}
-
-template <typename T, int D>
-hipError_t launch(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-    constexpr int RB = D * sizeof(T);
-    const unsigned units = (unsigned)a.d.C * a.d.Hkv * p.tiles * p.splits;
-    if constexpr (RB < 1024)
-        if (p.rows_per_group == kFewRows)
-            hipLaunchKernelGGL((attn_few_kernel<T, D>), dim3(units), dim3(64 * kFewWaves), 0, stream, a, p);
-    if constexpr (RB < 512 || sizeof(T) == 4)
-        if (p.rows_per_group == 64) launch_rows<T, D, 64>(a, p, units, stream);
-    if constexpr (RB < 512 && sizeof(T) == 2)
-        if (p.rows_per_group == 256) launch_rows<T, D, 256>(a, p, units, stream);
-    if constexpr (D == 256 && sizeof(T) == 2) {
-        if (p.rows_per_group == kPairRows)
-            hipLaunchKernelGGL((attn_pair_kernel<T>), dim3(p.tiles > 1 ? (units + 7) / 8 * 8 : units), dim3(kPairThreads), 0,
-                               stream, a, p);
-    } else if constexpr (RB < 1024) {
-        if (p.rows_per_group == 128) launch_rows<T, D, 128>(a, p, units, stream);
+    constexpr int W = D / 64, kAhead = 8;  // parts loaded together
+    typedef float vw __attribute__((ext_vector_type(W)));
+    typedef T tw __attribute__((ext_vector_type(W)));
+    const AttnDims &d = a.d;
+    const int lane = threadIdx.x & 63, parts = plan.splits;
+    const size_t all_rows = (size_t)d.C * d.N * d.Hq, row = (size_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
+    if (row >= all_rows) return;
+    const float *ml = join_pairs(a, plan) + row * 2, *po = a.workspace + row * D + lane * W;
+    vw v[kAhead];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            v[j] = *reinterpret_cast<const vw *>(po + (size_t)min(p0 + j, parts - 1) * all_rows * D);
+    };
+    load(0);
+    const float mine = ml[(size_t)min(lane, parts - 1) * all_rows * 2];
+    const float part_sum = lane < parts ? ml[(size_t)lane * all_rows * 2 + 1] : 0.f;
+    if (__builtin_amdgcn_ballot_w64(mine != mine)) return;  // an absent row
+    float mx = mine;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
+    // (a part without any attended row has weight 0; NaN sums stay NaN)
+    const float wgt = mine == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mine - mx);
+    float sum = part_sum == 0.f ? 0.f : part_sum * wgt;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k);
+    vw acc = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+        if (p0) load(p0);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const float w = p0 + j < parts ? __shfl(wgt, p0 + j) : 0.f;
+            if (w != 0.f) acc += v[j] * w;
+        }
     }
-    if (p.splits > 1) {
-        const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
-        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
-                           dim3(64 * kJoinWaves), 0, stream, a, p);
+    const int per = d.N * d.G, r = (int)(row % per), ch = (int)(row / per), h = ch % d.Hkv, c = ch / d.Hkv;
+    const int token = r / d.G, head = h * d.G + r - token * d.G;
+    const int64_t node = (int64_t)c * d.N + token;
+    acc = sum == 0.f ? vw(0.f) : acc / sum;
+    if (a.gate.p && sum != 0.f) {
+        const tw z = *reinterpret_cast<const tw *>(static_cast<const T *>(a.gate.p) + node * a.gate.token + head * a.gate.head + lane * W);
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] = gated(acc[i], (float)z[i], a.gate_mode);
     }
-    return hipGetLastError();
+    tw res;
+#pragma unroll
+    for (int i = 0; i < W; ++i) res[i] = (T)acc[i];
+    *reinterpret_cast<tw *>(static_cast<T *>(a.out) + (node * d.Hq + head) * D + lane * W) = res;
 }
 
 template <typename T>
-hipError_t launch_t(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-    if (a.d.D == 64) return launch<T, 64>(a, p, stream);
-    if (a.d.D == 128) return launch<T, 128>(a, p, stream);
-    return launch<T, 256>(a, p, stream);
+void launch_join(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    const size_t rows = (size_t)a.d.C * a.d.N * a.d.Hq;
+    const dim3 grid((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), block(64 * kJoinWaves);
+    if (a.d.D == 64)
+        hipLaunchKernelGGL((attn_join_kernel<T, 64>), grid, block, 0, stream, a, p);
+    else if (a.d.D == 128)
+        hipLaunchKernelGGL((attn_join_kernel<T, 128>), grid, block, 0, stream, a, p);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<T, 256>), grid, block, 0, stream, a, p);
 }
 
 }  // namespace
@@ -104,11 +115,18 @@ AttnPlan attn_plan(const AttnDims &d) {
     return p;
 }
 
+hipError_t launch_attention_join(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+    if (a.d.dtype == GDN_DTYPE_BF16)
+        launch_join<__bf16>(a, p, stream);
+    else if (a.d.dtype == GDN_DTYPE_F16)
+        launch_join<_Float16>(a, p, stream);
+    else
+        launch_join<float>(a, p, stream);
+    return hipGetLastError();
+}
+
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t stream) {
-    const AttnPlan p = attn_plan(a.d);
-    if (a.d.dtype == GDN_DTYPE_BF16) return launch_t<__bf16>(a, p, stream);
-    if (a.d.dtype == GDN_DTYPE_F16) return launch_t<_Float16>(a, p, stream);
-    return launch_t<float>(a, p, stream);
+    return launch_attention<false>(a, attn_plan(a.d), stream);
 }
 
 }  // namespace gdn

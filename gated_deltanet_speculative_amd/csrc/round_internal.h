@@ -79,6 +79,7 @@ inline size_t attn_workspace_floats(const AttnDims &d, const AttnPlan &p) {
 }
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t stream);
 hipError_t launch_paged_attention_kv4(const AttnArgs &a, hipStream_t stream);
+hipError_t launch_attention_join(const AttnArgs &a, const AttnPlan &p, hipStream_t stream);  // of the parts in the workspace
 
 struct CacheLayers {
     void *k[GDN_MAX_LAYERS], *v[GDN_MAX_LAYERS];

@@ -144,11 +144,11 @@ def kernel_of(name):
     m = re.search(r"\bgdn::.*?(\w+_kernel)(?:<([^>]*)>)?\(", name)
     if m:
         return f"{m[1]}<{m[2]}>" if m[2] else m[1]
-    m = re.match(r"_ZN3gdn12_GLOBAL__N_1\d+([a-z]\w*?_kernel)(?:I((?:DF16b|DF16_|f|Li\d+E)+)E)?", name)
+    m = re.match(r"_ZN3gdn12_GLOBAL__N_1\d+([a-z]\w*?_kernel)(?:I((?:DF16b|DF16_|f|Li\d+E|Lb[01]E)+)E)?", name)
     if not m:
         return None
-    types = {"DF16b": "bf16", "DF16_": "f16", "f": "float"}
-    args = [types.get(a) or a[2:-1] for a in re.findall(r"DF16b|DF16_|f|Li\d+E", m[2] or "")]
+    types = {"DF16b": "bf16", "DF16_": "f16", "f": "float", "Lb0E": "false", "Lb1E": "true"}
+    args = [types.get(a) or a[2:-1] for a in re.findall(r"DF16b|DF16_|f|Li\d+E|Lb[01]E", m[2] or "")]
     return f"{m[1]}<{', '.join(args)}>" if args else m[1]
 
 
