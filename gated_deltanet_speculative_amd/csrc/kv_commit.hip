@@ -13,6 +13,8 @@
 // verdict, and the preflight's entries are requested kBatch at a time.  4 lanes of 16 nodes, 16 layers of 8 heads of 128
 // in bfloat16: 6.5 us; 64 lanes of 32 nodes: 15.0 us; 4-bit caches of as many layers and heads: 6.8 and 16.8 us (a fourth of the
 // bytes, which did not bound it, and twice the arrays).
+#include <type_traits>
+
 #include "round_device.h"
 
 namespace gdn {
@@ -48,11 +50,12 @@ __device__ inline void store_bytes(char *p, v4i v) {
     if constexpr (B == 16) *reinterpret_cast<v4i *>(p) = v;
 }
 
-// kScales: bytes of a row's scales in a 4-bit cache (cl its codes, sc its scales), 0 without them (sc is cl)
+// kScales: bytes of a row's scales in a 4-bit cache, 0 for a cache of values
 template <int kScales>
-__device__ __forceinline__ void kv_commit(const AttnDims &d, int n_layers, const CacheLayers &cl, const CacheLayers &sc,
-                                          const PagedLanes &l, const int32_t *__restrict__ accept_node,
-                                          int32_t *__restrict__ new_len, int row_chunks) {
+__global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers,
+                                                             std::conditional_t<(kScales > 0), Cache4Layers, CacheLayers> cl,
+                                                             PagedLanes l, const int32_t *__restrict__ accept_node,
+                                                             int32_t *__restrict__ new_len, int row_chunks) {
     __shared__ unsigned s_bitmap[kBitmapSlots / 32];
     __shared__ int s_word, s_bits;
     __shared__ int s_slot[GDN_MAX_SEQS], s_len[GDN_MAX_SEQS], s_nodes[GDN_MAX_SEQS];  // slot -1: padding or in error
@@ -92,19 +95,24 @@ __device__ __forceinline__ void kv_commit(const AttnDims &d, int n_layers, const
     const int per = scales ? d.Hkv : cols, at = scales ? item - all : item, side = at / per, col = at - side * per;
     const bool mine = !lengths && side < 2 * n_layers;
     const int chunks = scales ? 1 : row_chunks;
-    const size_t row_bytes = scales ? kScales : 16 * (size_t)row_chunks;
+    const uint32_t row_bytes = scales ? kScales : 16 * row_chunks;
     char *p = nullptr;
     v4i v[kAhead];
     if (mine) {
-        const CacheLayers &of = scales ? sc : cl;
-        p = static_cast<char *>(side < n_layers ? of.k[side] : of.v[side - n_layers]) +
-            (size_t)(col / chunks) * d.page.d * row_bytes + 16 * (col % chunks);
+        void *array;
+        if constexpr (kScales > 0) {
+            const CacheLayers &of = scales ? cl.scales : cl.codes;
+            array = side < n_layers ? of.k[side] : of.v[side - n_layers];
+        } else {
+            array = side < n_layers ? cl.k[side] : cl.v[side - n_layers];
+        }
+        p = static_cast<char *>(array) + (size_t)(col / chunks) * d.page.d * row_bytes + 16 * (col % chunks);
     }
     auto load = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             if (j0 + j < n) {
-                const char *from = p + s_src[j0 + j] * row_bytes;
+                const char *from = p + (size_t)s_src[j0 + j] * row_bytes;
                 if (scales)
                     v[j] = load_bytes<kScales>(from);
                 else
@@ -178,25 +186,13 @@ __device__ __forceinline__ void kv_commit(const AttnDims &d, int n_layers, const
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             if (j0 + j < n) {
-                char *to = p + s_dst[j0 + j] * row_bytes;
+                char *to = p + (size_t)s_dst[j0 + j] * row_bytes;
                 if (scales)
                     store_bytes<kScales>(to, v[j]);
                 else
                     store_bytes<16>(to, v[j]);
             }
     }
-}
-
-__global__ __launch_bounds__(kThreads) void kv_commit_kernel(AttnDims d, int n_layers, CacheLayers cl, PagedLanes l,
-                                                             const int32_t *__restrict__ accept_node,
-                                                             int32_t *__restrict__ new_len, int row_chunks) {
-    kv_commit<0>(d, n_layers, cl, cl, l, accept_node, new_len, row_chunks);
-}
-template <int kScales>
-__global__ __launch_bounds__(kThreads) void kv4_commit_kernel(AttnDims d, int n_layers, Cache4Layers cl, PagedLanes l,
-                                                              const int32_t *__restrict__ accept_node,
-                                                              int32_t *__restrict__ new_len, int row_chunks) {
-    kv_commit<kScales>(d, n_layers, cl.codes, cl.scales, l, accept_node, new_len, row_chunks);
 }
 
 }  // namespace
@@ -208,7 +204,7 @@ hipError_t launch_kv_commit(const AttnDims &d, int n_layers, const CacheLayers &
     const int layers = l.parents ? n_layers : 0;
     const int row_chunks = d.D * es / 16;
     const int64_t items = 2ll * layers * d.Hkv * row_chunks;  // columns of a lane, one a thread
-    hipLaunchKernelGGL(kv_commit_kernel, dim3((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1),
+    hipLaunchKernelGGL(kv_commit_kernel<0>, dim3((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1),
                        dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     return hipGetLastError();
 }
@@ -220,11 +216,11 @@ hipError_t launch_kv4_commit(const AttnDims &d, int n_layers, const Cache4Layers
     const int64_t items = 2ll * layers * d.Hkv * (row_chunks + 1);
     const dim3 grid((unsigned)((items + kThreads - 1) / kThreads) + 1, l.parents ? d.C : 1);
     if (d.D == 64)
-        hipLaunchKernelGGL((kv4_commit_kernel<2>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+        hipLaunchKernelGGL((kv_commit_kernel<2>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     else if (d.D == 128)
-        hipLaunchKernelGGL((kv4_commit_kernel<4>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+        hipLaunchKernelGGL((kv_commit_kernel<4>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     else
-        hipLaunchKernelGGL((kv4_commit_kernel<8>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
+        hipLaunchKernelGGL((kv_commit_kernel<8>), grid, dim3(kThreads), 0, stream, d, layers, cl, l, accept_node, new_len, row_chunks);
     return hipGetLastError();
 }
 

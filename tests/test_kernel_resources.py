@@ -17,7 +17,7 @@ MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 # elsewhere, as these kernels had them over caches of values alone.
 MOST = {"attn_pair_kernelIDF16bLb0E": (148, 2), "attn_pair_kernelIDF16_Lb0E": (156, 1), "attn_rows_kernelIDF16bLi128ELi256ELb0E": (20, 244),
         "attn_rows_kernelIDF16_Li128ELi256ELb0E": (20, 242), "attn_rows_kernelIDF16bLi128ELi64ELb0E": (0, 241),
-        "attn_few_kernelIDF16bLi128ELb0E": (0, 107), "attn_few_kernelIfLi128ELb0E": (40, 22),
+        "attn_few_kernelIDF16bLi128ELb0E": (0, 107), "attn_few_kernelIfLi128ELb0E": (40, 22), "kv_commit_kernelILi0E": (0, 0),
         # and two forms of one kernel, neither of which costs the other anything
         "attn_pair_kernelIDF16bLb1E": (68, 1), "attn_pair_kernelIDF16_Lb1E": (76, 2)}
 

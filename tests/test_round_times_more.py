@@ -9,3 +9,4 @@ def test_names_of_kernels_with_switches():
         "attn_rows_kernel<f16, 128, 64, false>"
     assert T.kernel_of("void gdn::(anonymous namespace)::attn_few_kernel<float, 64, true>(gdn::AttnArgs, gdn::AttnPlan)") == \
         "attn_few_kernel<float, 64, true>"
+    assert T.kernel_of("void gdn::(anonymous namespace)::kv_commit_kernel<0>(gdn::AttnDims, int)") == "kv_commit_kernel<0>"
