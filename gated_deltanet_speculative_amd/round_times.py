@@ -4,7 +4,7 @@ gdn_logits.h calls over those of perf/more_operators.py.
     python -m gated_deltanet_speculative_amd.round_times [--more] [--only TEXT] [--further] [--draw N --seed S] [--plain] [--errors]
 
 Prints per case the microseconds of one pass among others (calls through the Python binding one after the other,
-over three sets of inputs in turn; the median of five loops) and the floor: the larger of bytes / the rate of a large
+over three sets of inputs in turn; the median of five loops) and the floor of these inputs: the larger of bytes / the rate of a large
 copy and operations / the rate of a large matrix product of the type, both measured first.  --further adds cases that
 the file does not list, --draw N cases drawn from its ranges with the given seed.  --plain also times the plain forms,
 --errors gives the distance from the definition in 64 bits (2-norm of the difference over that of the result).
@@ -96,6 +96,17 @@ def prepare(ops, case, seed):
         d[8] = entries
         s["dims"] = tuple(d)
     return s
+
+
+def work_of(ops, case, states):
+    """The case's work with the attended pairs of these inputs: their lanes have the case's lengths in another order, beside other
+    counts of nodes."""
+    w = dict(ops.work(case))
+    if case["op"] == "attn" and case["ragged"]:
+        counts, lens = ops._counts(case), [s["len"][s["slots"].long()].tolist() for s in states]
+        pairs = lambda of: sum(n * x for n, x in zip(counts, of))  # noqa: E731
+        w["flops"] += 4.0 * case["D"] * case["Hq"] * (statistics.mean(map(pairs, lens)) - pairs(ops._lens(case)))
+    return w
 
 
 def loop_us(run, passes, loops=5):
@@ -215,7 +226,7 @@ def main(argv=None):
             once = loop_us(run, 3, 1)
             line += f" {'here' if own else 'plain':5s} {loop_us(run, max(5, min(300, int(3e5 / once)))):9.1f} us"
         if rate:
-            w = ops.work(case)
+            w = work_of(ops, case, states)
             line += f"  floor {1e6 * max(w['bytes'] / rate['bytes'], w['flops'] / rate[case['dtype']]):7.1f} us"
         ops.own = True
         if a.errors:

@@ -1,6 +1,26 @@
-"""The timing tool: names of kernels with switches among their template arguments."""
+"""The timing tool over both files of cases: the work of the inputs that are run, and names of kernels with switches among their
+template arguments."""
+
+import pytest
+import torch
 
 from gated_deltanet_speculative_amd import round_times as T
+
+
+@pytest.mark.parametrize("more", [False, True])
+def test_work_is_that_of_the_inputs(more):
+    """Two chunks, lengths 16384 and 12288, nodes 2048 and 1536: the pairs by hand, with either length under either count."""
+    ops = T.operators(more)
+    case = next(c for c in ops.listed() if c["name"] == "attn chunk 2x2048 16k")
+    state = lambda *lens: dict(len=torch.tensor([5, lens[1], 7, lens[0]]), slots=torch.tensor([3, 1], dtype=torch.int32))  # noqa: E731
+    same, other = [(2048, 16384), (1536, 12288)], [(2048, 12288), (1536, 16384)]
+    flops = lambda lanes: 4.0 * 256 * 16 * sum(n * x + n * (n + 1) / 2 for n, x in lanes)  # noqa: E731
+    assert T.work_of(ops, case, [state(16384, 12288)]) == ops.work(case) and ops.work(case)["flops"] == flops(same)
+    assert T.work_of(ops, case, [state(12288, 16384)]) == dict(ops.work(case), flops=flops(other))
+    assert T.work_of(ops, case, [state(16384, 12288), state(12288, 16384)])["flops"] == (flops(same) + flops(other)) / 2
+    for c in ops.listed():
+        if not (c["op"] == "attn" and c["ragged"]):
+            assert T.work_of(ops, c, []) == ops.work(c)
 
 
 def test_names_of_kernels_with_switches():
