@@ -42,7 +42,7 @@ def kv4_cache(sh: R.AttnShape, device="cuda", layers=None) -> Kv4Cache:
 
 @functools.lru_cache(maxsize=1)
 def _library():
-    """The library with the prototypes of these calls."""
+    """The library with the prototypes of these calls, for callers through ctypes (the calls below go by their addresses)."""
     lib = load_library()
     sp = ctypes.POINTER(R._CAttnShape)
     lib.gdn_rope_kv4_write.argtypes = [sp, _i32, _vp, _vp, _vp, ctypes.POINTER(R._CRope)] + [_vp] * 9
@@ -56,27 +56,14 @@ def _library():
     return lib
 
 
-@functools.lru_cache(maxsize=None)
-def _call_of(name: str) -> tuple:
-    """The extension's function that makes a call, and the call's address in the library."""
-    return getattr(R._load_marshal(), name), ctypes.cast(getattr(_library(), "gdn_" + name), _vp).value
-
-
-@functools.lru_cache(maxsize=256)
-def _shape(sh) -> tuple:
-    """A shape's C struct (never written to), and its address."""
-    cs = sh.c_struct()
-    return cs, ctypes.addressof(cs)
-
-
 def rope_kv4_write(sh: R.AttnShape, q, k, v, inv_freq, cache, slot_ids, page_table, seq_len, positions=None, pair_axis=None,
                    parents=None, lane_nodes=None, q_norm=None, k_norm=None, eps=1e-6, interleaved=False, q_out=None,
                    status=None):
     """Rotary positions of q and k and the write of k and v, quantised to 4 bits, into the slots' pages behind their
     committed rows: rope_kv_write with a Kv4Cache in the place of the two caches.  Returns (q_out, status)."""
     device = R._device(q, "q")
-    call, f = _call_of("rope_kv4_write")
-    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    call, f = R._call_of("rope_kv4_write", _library)
+    held, shape = R._shape(sh)  # (held: the struct lives through the call)
     if q_out is None:
         q_out = torch.empty((sh.n_seqs, sh.n_nodes, sh.n_q_heads, sh.head_dim), dtype=sh.dtype, device=device)
     status = R._status_word(status, device)
@@ -87,7 +74,7 @@ def rope_kv4_write(sh: R.AttnShape, q, k, v, inv_freq, cache, slot_ids, page_tab
 
 def paged_attention_kv4_workspace_size(sh: R.AttnShape) -> int:
     """Bytes of device workspace paged_attention_kv4 needs for this shape (0 for an invalid shape)."""
-    return int(_library().gdn_paged_attention_kv4_workspace_size(ctypes.byref(_shape(sh)[0])))
+    return int(_library().gdn_paged_attention_kv4_workspace_size(ctypes.byref(R._shape(sh)[0])))
 
 
 def paged_attention_kv4(sh: R.AttnShape, q, cache, slot_ids, page_table, seq_len, parents=None, lane_nodes=None, scale=None,
@@ -95,8 +82,8 @@ def paged_attention_kv4(sh: R.AttnShape, q, cache, slot_ids, page_table, seq_len
     """Attention of the round's tokens over a 4-bit cache: paged_attention with a Kv4Cache in the place of the two
     caches (`workspace` is at least paged_attention_kv4_workspace_size(sh) bytes).  Returns (out, status)."""
     device = R._device(q, "q")
-    call, f = _call_of("paged_attention_kv4")
-    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    call, f = R._call_of("paged_attention_kv4", _library)
+    held, shape = R._shape(sh)  # (held: the struct lives through the call)
     if out is None:
         out = torch.empty((sh.n_seqs, sh.n_nodes, sh.n_q_heads, sh.head_dim), dtype=sh.dtype, device=device)
     status = R._status_word(status, device)
@@ -116,8 +103,8 @@ def kv4_commit_layers(sh: R.AttnShape, caches, slot_ids, page_table, seq_len, ac
     if status is None:
         raise ValueError("kv4_commit_layers needs a status word (the round's transaction flag)")
     device = R._device(status, "status")
-    call, f = _call_of("kv4_commit_layers")
-    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    call, f = R._call_of("kv4_commit_layers", _library)
+    held, shape = R._shape(sh)  # (held: the struct lives through the call)
     if new_len is None:
         new_len = torch.empty(sh.n_slots, dtype=torch.int32, device=device)
     R._call(device, call, "gdn_kv4_commit_layers", f, shape, device, caches, slot_ids, page_table,
@@ -139,8 +126,8 @@ def kv4_read_layers(sh: R.AttnShape, caches, slot_ids, page_table, first_row, la
     kv4_commit_layers).  Returns (k_out, v_out [layers, C, N, H_kv, D], status); rows that are absent (lane_nodes),
     of an offending lane or in a page outside the pool keep what k_out and v_out held (zeros if they are not given)."""
     device = R._device(slot_ids, "slot_ids")
-    call, f = _call_of("kv4_read_layers")
-    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    call, f = R._call_of("kv4_read_layers", _library)
+    held, shape = R._shape(sh)  # (held: the struct lives through the call)
     if k_out is None or v_out is None:
         rows = (_layers(caches), sh.n_seqs, sh.n_nodes, sh.n_kv_heads, sh.head_dim)
         k_out, v_out = (torch.zeros(rows, dtype=sh.dtype, device=device) if t is None else t for t in (k_out, v_out))

@@ -50,7 +50,7 @@ class LogitsShape(NamedTuple):
 
 @functools.lru_cache(maxsize=1)
 def _library():
-    """The library with the prototypes of these calls."""
+    """The library with the prototypes of these calls, for callers through ctypes (the calls below go by their addresses)."""
     lib = load_library()
     sp = ctypes.POINTER(_CLogitsShape)
     lib.gdn_adjust_logits.argtypes = [sp, _vp, ctypes.c_int64, ctypes.POINTER(_CLogitRules)] + [_vp] * 7 + [ctypes.c_size_t, _vp, _vp]
@@ -60,22 +60,9 @@ def _library():
     return lib
 
 
-@functools.lru_cache(maxsize=None)
-def _call_of(name: str) -> tuple:
-    """The extension's function that makes a call, and the call's address in the library."""
-    return getattr(R._load_marshal(), name), ctypes.cast(getattr(_library(), "gdn_" + name), _vp).value
-
-
-@functools.lru_cache(maxsize=256)
-def _shape(sh) -> tuple:
-    """A shape's C struct (never written to), and its address."""
-    cs = sh.c_struct()
-    return cs, ctypes.addressof(cs)
-
-
 def adjust_logits_workspace_size(sh: LogitsShape) -> int:
     """Bytes of device workspace adjust_logits needs for this shape where there is a temperature (0 for an invalid shape)."""
-    return int(_library().gdn_adjust_logits_workspace_size(ctypes.byref(_shape(sh)[0])))
+    return int(_library().gdn_adjust_logits_workspace_size(ctypes.byref(R._shape(sh)[0])))
 
 
 def adjust_logits(sh: LogitsShape, logits, slot_ids, history=None, history_len=None, prompt_len=None, repetition=None,
@@ -89,8 +76,8 @@ def adjust_logits(sh: LogitsShape, logits, slot_ids, history=None, history_len=N
     draft_accept takes.  `workspace` is a float32 device tensor of at least adjust_logits_workspace_size(sh) bytes
     (with a temperature; allocated per call when omitted).  Returns (out [C, N, V], status)."""
     device = R._device(logits, "logits")
-    call, f = _call_of("adjust_logits")
-    held, shape = _shape(sh)  # (held: the struct lives through the call)
+    call, f = R._call_of("adjust_logits", _library)
+    held, shape = R._shape(sh)  # (held: the struct lives through the call)
     if out is None:
         out = torch.empty((sh.n_seqs, sh.n_nodes, sh.vocab), dtype=sh.out_dtype, device=device)
     status = R._status_word(status, device)

@@ -183,6 +183,18 @@ def _cs(sh):
     return sh.c_struct()
 
 
+@functools.lru_cache(maxsize=256)
+def _shape(sh) -> tuple:
+    """A shape's C struct, and its address (for the calls that the extension makes)."""
+    return _cs(sh), ctypes.addressof(_cs(sh))
+
+
+@functools.lru_cache(maxsize=None)
+def _call_of(name: str, library) -> tuple:
+    """The extension's function that makes a call, and the call's address in library()."""
+    return getattr(_load_marshal(), name), ctypes.cast(getattr(library(), "gdn_" + name), _vp).value
+
+
 def _places(sh: AttnShape, slot_ids, page_table, seq_len, device) -> tuple:
     return (_ptr(slot_ids, "slot_ids", torch.int32, (sh.n_seqs,), device),
             _ptr(page_table, "page_table", torch.int32, (sh.n_slots, sh.max_pages), device),

@@ -17,24 +17,8 @@ constexpr int kAhead = 4;     // rows of a thread that are requested together
 
 template <typename T>
 __device__ inline void four_out(T *p, int w, unsigned scale) {
-    const float s = __uint_as_float(scale << 23);
-    if constexpr (sizeof(T) == 4) {
-        typedef float f2 __attribute__((ext_vector_type(2)));
-        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-        const f2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-        *reinterpret_cast<v4f *>(p) = v4f{a[0], a[1], b[0], b[1]};
-        *reinterpret_cast<v4f *>(p + 4) = v4f{c[0], c[1], d[0], d[1]};
-    } else if constexpr (__is_same(T, __bf16)) {
-        *reinterpret_cast<v4i *>(p) = v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
-    } else {
-        *reinterpret_cast<v4i *>(p) = v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
-                                          __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
-    }
+#pragma unroll
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) reinterpret_cast<v4i *>(p)[h] = four_values<T>(w, scale, h);
 }
 
 // Grid: (tokens / kTokens, lanes, 2 layers + (K or V)).

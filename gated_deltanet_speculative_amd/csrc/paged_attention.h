@@ -282,31 +282,6 @@ __device__ inline void leave_nothing(const AttnArgs &a, const AttnPlan &plan, in
 }
 
 // ---- 4-bit rows: D / 2 bytes of codes, the lower nibble first, and D / 32 bytes of scales
-// The 8 codes of a word as values of T: one operand of 16 bytes for 16-bit types, half h of them (4 values) for float.
-// The conversion instruction multiplies by the power of two; byte 255 (as 2^128, an infinity) gives NaN.
-template <typename T>
-__device__ inline v4i four_values(int w, unsigned scale, int h) {
-    const float s = __builtin_bit_cast(float, scale << 23);
-    v4i r;
-    if constexpr (std::is_same_v<T, __bf16>) {
-        r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-        r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-        r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-        r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-    } else if constexpr (std::is_same_v<T, _Float16>) {
-        r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
-        r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
-        r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
-        r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
-    } else {
-        typedef float f2 __attribute__((ext_vector_type(2)));
-        const unsigned half = (unsigned)w >> (16 * h);
-        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(half, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(half, s, 1);
-        r = __builtin_bit_cast(v4i, v4f{a[0], a[1], b[0], b[1]});
-    }
-    return r;
-}
-
 // B bytes of codes of a row (8: half a block of 32 values, 16: a block) and their scale
 template <int B>
 struct Codes {

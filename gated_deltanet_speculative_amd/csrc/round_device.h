@@ -2,6 +2,8 @@
 // the place of a cache row.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_device.h"
 #include "round_internal.h"
 
@@ -66,6 +68,31 @@ __device__ inline bool slot_shared(const int32_t *__restrict__ slot_ids, int C, 
 // Row number (in units of D values) of place `t % page_size` of page `pid` for kv head h.
 __device__ inline uint32_t cache_row(const AttnDims &d, int pid, int h, uint32_t t, uint32_t entry) {
     return ((uint32_t)pid * d.Hkv + h) * d.page.d + (t - entry * d.page.d);
+}
+
+// 4-bit rows: the 8 codes of a word as values of T: one operand of 16 bytes for 16-bit types, half h of them (4 values) for float.
+// The conversion instruction multiplies by the power of two; byte 255 (as 2^128, an infinity) gives NaN.
+template <typename T>
+__device__ inline v4i four_values(int w, unsigned scale, int h) {
+    const float s = __builtin_bit_cast(float, scale << 23);
+    v4i r;
+    if constexpr (std::is_same_v<T, __bf16>) {
+        r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+        r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+        r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+        r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+    } else if constexpr (std::is_same_v<T, _Float16>) {
+        r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+        r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+        r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+        r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+    } else {
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const unsigned half = (unsigned)w >> (16 * h);
+        const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(half, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(half, s, 1);
+        r = __builtin_bit_cast(v4i, v4f{a[0], a[1], b[0], b[1]});
+    }
+    return r;
 }
 
 }  // namespace gdn
