@@ -68,6 +68,40 @@ FURTHER_MORE = [
          ragged=False, gate=False),
     dict(name="attn chain 5x8 f32 256", op="attn", C=5, N=8, Hq=8, Hkv=8, D=256, ctx=2999, page=48, dtype="f32", tree=False,
          ragged=True, gate=False),
+    # a page table for 128k rows over a short cache, and over one of 8192 tokens
+    dict(name="attn decode 1x1k, table of 128k", op="attn", C=1, N=1, Hq=16, Hkv=2, D=128, ctx=1003, page=16, dtype="bf16",
+         tree=False, ragged=False, gate=False, rows=1 << 17),
+    dict(name="attn tree 4x16 1k, table of 128k", op="attn", C=4, N=16, Hq=32, Hkv=8, D=128, ctx=1000, page=64, dtype="bf16",
+         tree=True, ragged=False, gate=False, rows=1 << 17),
+    dict(name="attn tree 1x16 8k, table of 128k", op="attn", C=1, N=16, Hq=32, Hkv=8, D=128, ctx=8192, page=64, dtype="bf16",
+         tree=True, ragged=False, gate=False, rows=1 << 17),
+    # more than 16 query rows in float32
+    dict(name="attn tree 4x16 8k f32", op="attn", C=4, N=16, Hq=32, Hkv=8, D=128, ctx=8192, page=64, dtype="f32", tree=True,
+         ragged=False, gate=False),
+    dict(name="attn tree 4x16 8k f32 256", op="attn", C=4, N=16, Hq=24, Hkv=4, D=256, ctx=8192, page=64, dtype="f32", tree=True,
+         ragged=False, gate=False),
+    dict(name="attn chunk 1x1024 4k f32", op="attn", C=1, N=1024, Hq=16, Hkv=4, D=64, ctx=4096, page=64, dtype="f32", tree=False,
+         ragged=False, gate=False),
+    # chunks of the narrower heads, and prompts into an empty cache
+    dict(name="attn chunk 2x2048 16k, 128", op="attn", C=2, N=2048, Hq=32, Hkv=8, D=128, ctx=16384, page=64, dtype="bf16",
+         tree=False, ragged=False, gate=False),
+    dict(name="attn chunk 2x2048 16k, 64", op="attn", C=2, N=2048, Hq=32, Hkv=8, D=64, ctx=16384, page=64, dtype="f16", tree=False,
+         ragged=False, gate=False),
+    dict(name="attn prompt 1x4096", op="attn", C=1, N=4096, Hq=32, Hkv=8, D=128, ctx=0, page=64, dtype="bf16", tree=False,
+         ragged=False, gate=False),
+    dict(name="attn prompt 1x1417, 64", op="attn", C=1, N=1417, Hq=8, Hkv=8, D=64, ctx=0, page=64, dtype="bf16", tree=False,
+         ragged=False, gate=False),
+    dict(name="attn prompt 1x1164, 256", op="attn", C=1, N=1164, Hq=9, Hkv=3, D=256, ctx=0, page=64, dtype="bf16", tree=False,
+         ragged=False, gate=False),
+    # many rows of logits, and vocabularies within one stretch
+    dict(name="logits tree 32x32, no temperature", op="logits", C=32, N=32, V=130001, history=8192, bias=300, mask=True, tokens=True,
+         tree=True, temp=False, ragged=False, dtype="bf16", out="bf16"),
+    dict(name="logits tree 32x32", op="logits", C=32, N=32, V=130001, history=8192, bias=300, mask=True, tokens=True, tree=True,
+         temp=True, ragged=False, dtype="bf16", out="f32"),
+    dict(name="logits tree 52x32 small", op="logits", C=52, N=32, V=1092, history=2000, bias=20, mask=True, tokens=True, tree=True,
+         temp=True, ragged=False, dtype="bf16", out="f32"),
+    dict(name="logits chain 1x22 small", op="logits", C=1, N=22, V=1220, history=24000, bias=20, mask=True, tokens=True, tree=False,
+         temp=True, ragged=False, dtype="bf16", out="f32"),
 ]
 
 
@@ -153,8 +187,9 @@ def kernel_of(name):
     """Name and template arguments of one of this library's kernels, else None; a profiler leaves the names with 16-bit types
     mangled."""
     m = re.search(r"\bgdn::.*?(\w+_kernel)(?:<([^>]*)>)?\(", name)
-    if m:
-        return f"{m[1]}<{m[2]}>" if m[2] else m[1]
+    if m:  # (a demangler that does not know bfloat16 takes it for another type, with the argument behind it)
+        args = (m[2] or "").replace("bool _Accum, bool, E", "bf16, true").replace("bool _Accum", "bf16, float")
+        return f"{m[1]}<{args}>" if args else m[1]
     m = re.match(r"_ZN3gdn12_GLOBAL__N_1\d+([a-z]\w*?_kernel)(?:I((?:DF16b|DF16_|f|Li\d+E|Lb[01]E)+)E)?", name)
     if not m:
         return None

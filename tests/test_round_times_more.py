@@ -23,6 +23,15 @@ def test_work_is_that_of_the_inputs(more):
             assert T.work_of(ops, c, []) == ops.work(c)
 
 
+def test_further_cases_are_complete():
+    ops = T.operators(True)
+    got = T.cases(ops, further=True)
+    assert len({c["name"] for c in got}) == len(got) == len(ops.listed()) + len(T.FURTHER_MORE)
+    keys = {c["op"]: set(c) for c in ops.listed()}
+    for c in T.FURTHER_MORE:
+        assert set(c) - {"rows"} == keys[c["op"]] and ops.work(c)["bytes"] > 0, c["name"]
+
+
 def test_names_of_kernels_with_switches():
     assert T.kernel_of("_ZN3gdn12_GLOBAL__N_116attn_pair_kernelIDF16bLb1EEEvNS_8AttnArgsENS_8AttnPlanE") == "attn_pair_kernel<bf16, true>"
     assert T.kernel_of("_ZN3gdn12_GLOBAL__N_116attn_rows_kernelIDF16_Li128ELi64ELb0EEEvNS_8AttnArgsENS_8AttnPlanE") == \
@@ -30,3 +39,6 @@ def test_names_of_kernels_with_switches():
     assert T.kernel_of("void gdn::(anonymous namespace)::attn_few_kernel<float, 64, true>(gdn::AttnArgs, gdn::AttnPlan)") == \
         "attn_few_kernel<float, 64, true>"
     assert T.kernel_of("void gdn::(anonymous namespace)::kv_commit_kernel<0>(gdn::AttnDims, int)") == "kv_commit_kernel<0>"
+    misread = "void gdn::(anonymous namespace)::{}_kernel<bool _Accum, {}>(gdn::LogitArgs)"
+    assert T.kernel_of(misread.format("adjust_logits", "2")) == "adjust_logits_kernel<bf16, float, 2>"
+    assert T.kernel_of(misread.format("attn_pair", "bool, E")) == "attn_pair_kernel<bf16, true>"
