@@ -133,8 +133,8 @@ __device__ inline int swizzle(int r) {
 // kTurned: for a 4-bit cache's tile of 16-bit values, whose lanes write several chunks in a row each: eight lanes write at a
 // time, to 32 banks, and would share them two or four at a time, as all are at the same one of their chunks.  So
 // chunks are placed one (and two) further along by the bits of their number (a row of 128 bytes: the row's) that tell
-// those lanes apart; what is read together has the same such bits.  (Without: 8 to 24 cycles more a write, 44% of the LDS time of
-// chunks at D = 256.)
+// those lanes apart; what is read together has the same such bits.  (Without: 44% of the LDS time of chunks at
+// D = 256 are conflicts, 23% of that of trees of 64 rows at D = 128; the chunks 1499 us and 1241.)
 template <int kRowBytes, bool kTurned = false>
 __device__ inline int lds_at(int r, int chunk) {
     int at = chunk ^ swizzle<kRowBytes>(r);
@@ -742,7 +742,7 @@ __global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) 
 // query rows: each computes the scores of one half of a tile's 64 cache rows against the whole width, the pair
 // exchanges its rows' maxima and the weights (8 KiB a tile through LDS), and each multiplies all of the weights with
 // its half of the columns of V.  Per product a wave reads half as much LDS as with 16 rows, and holds 64 registers
-// of outputs.  Chunks of 2 x 2048 tokens behind 16k (16 / 2 heads, bfloat16) take 1269 us, 719 TFLOP/s (a wave with 16 rows:
+// of outputs.  Chunks of 2 x 2048 tokens behind 16k (16 / 2 heads, bfloat16) take 1277 us, 697 TFLOP/s (a wave with 16 rows:
 // 1544 us); the matrix pipes are busy 37% of the time, and the two barriers keep the eight waves in step, so that
 // products and softmax overlap little.  Two barriers a tile: behind the maxima, where K has been read and V of the tile is written, and behind
 // the weights, where K of the next tile is.
@@ -1105,7 +1105,7 @@ GDN_ATTN_PAIR(AttnArgs a, AttnPlan plan) {
 // 510 us); one lane behind 1003 tokens: 7 us, and 3.2 us for the join.
 //
 // A 4-bit cache has a fourth of the bytes for as many rows: a tile is 16 KiB of V as values (at most 64 rows), so that
-// a wave has 2 to 4 KiB of K and of V in flight.  The same 64 lanes over it, 864 MB: 178 us, 4.85 TB/s, 94% of a copy (lanes of
+// a wave has 2 to 4 KiB of K and of V in flight.  The same 64 lanes over it, 864 MB: 179 us, 4.8 TB/s, 94% of a copy (lanes of
 // equal length 158 us, 5.45 TB/s: the last workgroups of a ragged batch run alone); one lane behind 1003 tokens: 7.6 us.  Tiles
 // of 8 KiB in three workgroups a CU: 175 us; two tiles in flight: 177.
 constexpr int kFewWaves = 4, kFewRows = 16;
