@@ -172,8 +172,6 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
     __shared__ __attribute__((aligned(16))) unsigned s_word[kChunk];
     __shared__ __attribute__((aligned(16))) float s_bias[kChunk];
     __shared__ int s_again;
-    __shared__ __attribute__((aligned(16))) int s_list[kMostBiases];  // the slot's biases, where a token has several
-    __shared__ __attribute__((aligned(16))) float s_value[kMostBiases];
     __shared__ unsigned s_anc[GDN_MAX_NODES];
     __shared__ Total s_total[GDN_MAX_NODES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = blockIdx.y, x0 = blockIdx.x * kChunk;
@@ -324,22 +322,18 @@ __global__ __launch_bounds__(kThreads, 4) void adjust_logits_kernel(LogitArgs a)
     }
     lds_barrier();
     // Tokens with several biases: the wave that was first at one finds its entries and adds them, in the list's order (1024 biases, 4
-    // rows of 32768: one token twice 5.1 us and 4.4 without, all of one token 38; each entry's thread going through the list in
-    // memory 207 and 202).
+    // rows of 32768: one token twice 5.4 us and 4.4 without, all of one token 37; each entry's thread going through the list
+    // 207 and 202).  The list comes from memory again: with a copy in LDS, 8 KiB, a workgroup fewer fits a CU (32 x 32 rows of 130001
+    // without a temperature 151 us and 140).
     if (biased && s_again) {
-#pragma unroll
-        for (int j = 0; j < kBiases; ++j) {
-            const int at = j * kThreads + tid;
-            s_list[at] = at < a.B ? bias_tok[j] : -1;
-            if (at < a.B) s_value[at] = bias_val[j];
-        }
-        lds_barrier();
         int t[kMostBiases / 64];  // entries 64 i + lane
         float v[kMostBiases / 64];
 #pragma unroll
         for (int i = 0; i < kMostBiases / 64; ++i) {
-            t[i] = s_list[64 * i + lane];
-            v[i] = s_value[64 * i + lane];
+            const int64_t at = (int64_t)slot * a.B + min(64 * i + lane, a.B - 1);
+            t[i] = a.r.bias_tokens[at];
+            v[i] = a.r.bias[at];
+            if (64 * i + lane >= a.B) t[i] = -1;
         }
 #pragma unroll
         for (int j = 0; j < kBiases; ++j) {
