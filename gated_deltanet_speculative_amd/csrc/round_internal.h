@@ -58,13 +58,13 @@ hipError_t launch_rope_kv_write(const RopeArgs &a, hipStream_t stream);
 struct AttnArgs {
     AttnDims d;
     PagedLanes l;
-    const void *q, *k_cache, *v_cache;  // a 4-bit cache's codes
-    const void *k_scales, *v_scales;    // and its scales, else null
+    const void *q, *k_cache, *v_cache;  // (a 4-bit cache: its codes)
     float scale_log2;  // scale * log2(e)
     HeadsView gate;    // p null: no gate
     int gate_mode;
     void *out;
     float *workspace;
+    const void *k_scales, *v_scales;  // of a 4-bit cache, else null
 };
 // How the rows and the cache of a call are divided over workgroups, by the shape alone.
 struct AttnPlan {
