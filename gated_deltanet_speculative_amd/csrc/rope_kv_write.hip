@@ -85,8 +85,11 @@ __device__ inline Quantised quantised(const float (&x)[8]) {
 
 constexpr int kAhead = 3;  // rounds of rows requested together: 48 rows of 128, 24 of 256
 
+// Over 4 bits four workgroups a CU, as the other has by itself (as this was chosen, 2 x 4096 tokens with 141 registers 94 us and with
+// 128 78): from float32 two registers are in memory at D = 64 and 128.  The text is the kernel itself: as a function that the
+// kernels call, the prompt takes 66.2 us and 65.4 over values, and with its rows read 83.1 and 76.2 over 4 bits.
 template <typename X, typename T, int D, bool kFour>
-__device__ __forceinline__ void rope_kv_write(const RopeArgs &a) {
+__global__ __launch_bounds__(kThreads, kFour ? 4 : 1) void rope_kv_write_kernel(RopeArgs a) {
     constexpr int LPR = D / 8, RPB = kThreads / LPR;  // lanes per head row, rows a workgroup carries at a time
     __shared__ float s_cos[2][D / 2], s_sin[2][D / 2];
     __shared__ int s_bits;
@@ -212,22 +215,11 @@ __device__ __forceinline__ void rope_kv_write(const RopeArgs &a) {
 }
 
 template <typename X, typename T, int D>
-__global__ __launch_bounds__(kThreads) void rope_kv_write_kernel(RopeArgs a) {
-    rope_kv_write<X, T, D, false>(a);
-}
-// (four workgroups a CU, as the other has by itself: with 141 registers instead of 128, 2 x 4096 tokens took 94 us; from float32 to
-// 16 bits two registers are in memory)
-template <typename X, typename T, int D>
-__global__ __launch_bounds__(kThreads, 4) void rope_kv4_write_kernel(RopeArgs a) {
-    rope_kv_write<X, T, D, true>(a);
-}
-
-template <typename X, typename T, int D>
 void launch_d(const RopeArgs &a, dim3 grid, hipStream_t stream) {
     if (a.k_scales)
-        hipLaunchKernelGGL((rope_kv4_write_kernel<X, T, D>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((rope_kv_write_kernel<X, T, D, true>), grid, dim3(kThreads), 0, stream, a);
     else
-        hipLaunchKernelGGL((rope_kv_write_kernel<X, T, D>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((rope_kv_write_kernel<X, T, D, false>), grid, dim3(kThreads), 0, stream, a);
 }
 
 template <typename X, typename T>
