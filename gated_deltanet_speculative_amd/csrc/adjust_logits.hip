@@ -12,12 +12,12 @@
 // it in 32 bits and reading that).  Bound by bytes where there are many rows, by the chain slot, history,
 // LDS, logits and by launches where there are few.
 //
-// 4 lanes of 16 nodes, 130001 tokens, every rule, bfloat16 to float32 probabilities: 15.5 + 16.2 us for 17 and 17 + 33 MB (some
+// 4 lanes of 16 nodes, 130001 tokens, every rule, bfloat16 to float32 probabilities: 15.5 + 16.3 us for 17 and 17 + 33 MB (some
 // 5 us of each until the first row is worked on, then about 15 operations and an exponential a value); 32 lanes of 32:
-// 347 us, 3.2 TB/s over both launches, and without a temperature, to bfloat16, 152 us, 3.6 TB/s; one node of 4 lanes, 32768
+// 348 us, 3.2 TB/s over both launches, and without a temperature, to bfloat16, 140 us, 3.9 TB/s; one node of 4 lanes, 32768
 // tokens, bfloat16 logits: 5.2 us.  Eight tokens a thread and
 // 512 threads: with 16 and 256 the constants of a thread's tokens went through memory (54.6 us and 44).  Two rows in flight
-// instead of one: 30.7 us and 30.3, 32 lanes of 32 369 and 352.
+// instead of one: 30.7 us and 30.3, 32 lanes of 32 369 and 352 (as this was chosen).
 #include "logits_internal.h"
 #include "round_device.h"
 

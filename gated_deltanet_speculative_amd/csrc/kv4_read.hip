@@ -5,7 +5,7 @@
 // either K or V, and finds its tokens' pages first, one thread a token; four rows of a thread are in flight.
 //
 // 4095 rows of 16 layers, 8 heads of 128, float16: 70 us, 4.9 TB/s (K and V in one workgroup, one row of a thread at a time: 76);
-// 64 lanes of 32 rows of 16 layers, 8 heads of 128: 40.5 us, 4.2 TB/s (46.6); 64 rows of a layer: 4.3 us (6.8).
+// 64 lanes of 32 rows of 16 layers, 8 heads of 128: 41.1 us, 4.1 TB/s (46.6); 64 rows of a layer: 4.0 us (6.8).
 #include "round_device.h"
 
 namespace gdn {

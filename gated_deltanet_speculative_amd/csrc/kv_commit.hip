@@ -11,7 +11,7 @@
 // Bound by launch and by dependent reads (slot, length, page id, row): every workgroup checks all lanes itself, as
 // in the replay commit, so one launch decides; its own rows are found and the first of them loaded ahead of the
 // verdict, and the preflight's entries are requested kBatch at a time.  4 lanes of 16 nodes, 16 layers of 8 heads of 128
-// in bfloat16: 6.3 us; 64 lanes of 32 nodes: 14.8 us; 4-bit caches of as many layers and heads: 6.7 and 17.0 us (a fourth of the
+// in bfloat16: 6.2 us; 64 lanes of 32 nodes: 14.9 us; 4-bit caches of as many layers and heads: 6.8 and 16.6 us (a fourth of the
 // bytes, which did not bound it, and twice the arrays).
 #include <type_traits>
 

@@ -134,7 +134,7 @@ __device__ inline int swizzle(int r) {
 // time, to 32 banks, and would share them two or four at a time, as all are at the same one of their chunks.  So
 // chunks are placed one (and two) further along by the bits of their number (a row of 128 bytes: the row's) that tell
 // those lanes apart; what is read together has the same such bits.  (Without: 44% of the LDS time of chunks at
-// D = 256 are conflicts, 23% of that of trees of 64 rows at D = 128; the chunks 1499 us and 1241.)
+// D = 256 are conflicts, 23% of that of trees of 64 rows at D = 128; the chunks 1472 us and 1226.)
 template <int kRowBytes, bool kTurned = false>
 __device__ inline int lds_at(int r, int chunk) {
     int at = chunk ^ swizzle<kRowBytes>(r);
@@ -749,8 +749,8 @@ __global__ __launch_bounds__(64 * group_waves(BM), group_blocks(sizeof(T), BM)) 
 constexpr int kPairRows = 128, kPairThreads = 512;
 
 // The text below is the kernel itself over 16 bits, and a function that the kernel calls over 4: the registers that the compiler
-// keeps in memory are others, by no rule to be seen from here (the chunks above as kernel and as function: over 16 bits 1277 us
-// and 1290, over 4 bits 1290 and 1248).
+// keeps in memory are others, by no rule to be seen from here (as this was chosen, the chunks above as kernel and as
+// function: over 16 bits 1277 us and 1290, over 4 bits 1290 and 1248).
 template <typename T, bool kFour>
 __global__ void attn_pair_kernel(AttnArgs a, AttnPlan plan);
 #ifndef GDN_ATTN_PAIR

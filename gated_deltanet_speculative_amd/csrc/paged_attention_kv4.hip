@@ -3,9 +3,9 @@
 // over them, and their launches.
 //
 // What bounds them: many query rows the products and the softmax, as over 16 bits (two chunks of 2048 behind 16k, D = 256,
-// bfloat16: 1241 us, 717 TFLOP/s, and 1277 over a 16-bit cache); 17 to 64 rows the tiles' chain of load, conversion, LDS
+// bfloat16: 1226 us, 726 TFLOP/s, and 1277 over a 16-bit cache); 17 to 64 rows the tiles' chain of load, conversion, LDS
 // and products, with two waves a SIMD to cover it (trees of 4 x 16 nodes behind 8192, 32 / 8 heads of 128: 24 us for 19 MB
-// and 8.6 GFLOP, and 5.6 for the join; over 16 bits 36); few rows the bytes.
+// and 8.6 GFLOP, and 5.4 for the join; over 16 bits 36); few rows the bytes.
 #define GDN_ATTN_PAIR __device__ __forceinline__ void attn_pair
 #include "paged_attention.h"
 

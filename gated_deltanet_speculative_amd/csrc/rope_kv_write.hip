@@ -20,7 +20,7 @@
 // instruction rounds the codes to nearest even and saturates.
 //
 // 2 x 4096 tokens, 16 + 2 + 2 heads of 256, three axes, norms, float32 to bfloat16: 65.3 us, 3.9 TB/s (a copy of as many
-// bytes 53 us); 4 tokens of 32 + 8 + 8 heads of 128: 5.9 us.  The same into a 4-bit cache: 77.8 us, 3.0 TB/s (a copy 47 us; the
+// bytes 53 us); 4 tokens of 32 + 8 + 8 heads of 128: 5.9 us.  The same into a 4-bit cache: 71.8 us, 3.3 TB/s (a copy 47 us; the
 // waves that quantise take longest, and the rotation's work is no less for fewer bytes), and 6.0 us.
 #include <type_traits>
 
